@@ -1,7 +1,8 @@
 /*
  * moe_ffn.h - C ABI of libmoe_ffn.so: forward pass of a mixture-of-experts
  * feed-forward layer with fine-grained routed experts and an always-on shared
- * expert, on one NVIDIA B200 (sm_100a).
+ * expert, on one NVIDIA B200 (sm_100a); and the operators a block around it is
+ * trained with (norm, gated feed-forward block, dropout, with their gradients).
  *
  * What the library computes (one call of moe_forward, T tokens of width d):
  *
@@ -295,6 +296,99 @@ void moe_plan_destroy(moe_plan_t plan);
 
 const char* moe_strerror(int status);
 const char* moe_last_error(void);
+
+/* ------------------------------------------------------------------------
+ * Operators around the layer, with their gradients: norm, gated feed-forward
+ * block, dropout with the residual add. They need no plan. They launch on the
+ * calling thread's current CUDA device, which must own the tensors and the
+ * stream; they keep nothing between calls, so calls on different streams (or
+ * threads) are independent as long as their workspaces are. Row strides (ld*)
+ * count elements. Outputs must not overlap inputs unless stated.
+ * ------------------------------------------------------------------------ */
+enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_FP16 = 1, MOE_DTYPE_FP32 = 2 };
+enum { MOE_NORM_LAYER = 0, MOE_NORM_RMS = 1 };
+enum { MOE_ACT_SILU = 0, MOE_ACT_GELU = 1 };
+
+/* Norm over the rows of x (rows, cols):
+ *   MOE_NORM_LAYER: xh = (x - mean) * rstd, rstd = 1 / sqrt(mean((x - mean)^2) + eps)
+ *   MOE_NORM_RMS:   xh = x * rstd,          rstd = 1 / sqrt(mean(x^2) + eps)
+ *   y = xh * weight + bias
+ * ("Shared Expert (DeepSeek-V3)", "How it works": the layer's input is already
+ * RMS-normalised.) weight (cols) and bias (cols) may be NULL (1 and 0) and have
+ * x's dtype or fp32 (wdtype); an RMS norm takes no bias. mean and rstd (rows,
+ * fp32) are written when non-NULL, for the backward pass (mean: layer norm
+ * only). Any cols up to 2^24, any row strides >= cols, any element-aligned
+ * pointers; 16-byte aligned rows run faster. y may be x itself (equal strides). */
+int moe_norm_forward(int kind, int dtype, int wdtype, int64_t rows, int64_t cols,
+                     const void* x, int64_t ldx, const void* weight, const void* bias,
+                     double eps, void* y, int64_t ldy, float* mean, float* rstd,
+                     void* stream);
+
+/* Backward of moe_norm_forward, with the mean and rstd it wrote:
+ *   g = dy * weight,  dx = rstd * (g - mean(g) - xh * mean(g * xh))  (RMS: without mean(g))
+ *   dweight = sum over rows of dy * xh,  dbias = sum over rows of dy
+ * dx, dweight and dbias may be NULL (not computed); dweight and dbias have
+ * wdtype. The workspace (16-byte aligned, moe_norm_workspace_bytes) is needed
+ * for dweight or dbias. Sums run in a fixed order: equal inputs, equal bits.
+ * With rows = 0, dweight and dbias are set to zero. dx may be dy itself (equal
+ * strides). */
+size_t moe_norm_workspace_bytes(int kind, int64_t rows, int64_t cols);
+int moe_norm_backward(int kind, int dtype, int wdtype, int64_t rows, int64_t cols,
+                      const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                      const void* weight, const float* mean, const float* rstd, void* dx,
+                      int64_t lddx, void* dweight, void* dbias, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
+/* Gated feed-forward block over T tokens (the shared expert of the layer, or a
+ * dense feed-forward layer):
+ *   gate = x W1^T,  up = x W3^T,  h = act(gate) * up,  out = h W2^T
+ * x (T, d), W1 and W3 (f, d), W2 (d, f) contiguous, out (T, d); bf16 or fp16,
+ * fp32 accumulation, h rounded to the type between the two products. act is
+ * SiLU, or GELU in its tanh form. gate and up (T, f), both or neither, receive
+ * the pre-activations for the backward pass. d and f are multiples of 8; row
+ * strides are multiples of 8; pointers are 16-byte aligned; the workspace is
+ * 256-byte aligned, moe_gated_ffn_workspace_bytes(T, d, f, 0) bytes. */
+size_t moe_gated_ffn_workspace_bytes(int64_t T, int64_t d, int64_t f, int backward);
+int moe_gated_ffn_forward(int act, int dtype, int64_t T, int64_t d, int64_t f,
+                          const void* x, int64_t ldx, const void* W1, const void* W3,
+                          const void* W2, void* out, int64_t ldo, void* gate, void* up,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
+/* Backward of moe_gated_ffn_forward from dout (T, d) and the saved gate and up:
+ *   dh = dout W2,  dgate = dh * up * act'(gate),  dup = dh * act(gate)
+ *   dx = dgate W1 + dup W3,  dW1 = dgate^T x,  dW3 = dup^T x,  dW2 = dout^T h
+ * Any of dx, dW1, dW3, dW2 may be NULL (not computed); the weight gradients are
+ * contiguous, overwritten (zero when T = 0). dgate, dup and h are rounded to
+ * the type between the products. Workspace as above with backward = 1. */
+int moe_gated_ffn_backward(int act, int dtype, int64_t T, int64_t d, int64_t f,
+                           const void* dout, int64_t lddout, const void* x, int64_t ldx,
+                           const void* W1, const void* W3, const void* W2, const void* gate,
+                           const void* up, void* dx, int64_t lddx, void* dW1, void* dW3,
+                           void* dW2, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Residual add with dropout: out[e] = residual[e] + (keep(e) ? x[e] / (1 - p) : 0)
+ * (residual NULL: 0), e = row * cols + column. keep(e) holds when word e % 4 of
+ * Philox-4x32-10 with the 128-bit counter (low 64 bits e / 4, high 64 bits
+ * offset) and the key seed is at least round(p * 2^32). rng points to two
+ * uint64 in DEVICE memory, the seed and the offset, read when the kernel runs:
+ * a captured graph draws anew when the program changes them between replays.
+ * The mask is not stored; the backward pass draws it again from the same seed
+ * and offset: dx[e] = keep(e) ? dout[e] / (1 - p) : 0 (the residual's gradient
+ * is dout). A dropped element adds exactly 0, also where x is not finite. p in
+ * [0, 1]; rng may be NULL when p = 0. Any strides >= cols and any
+ * element-aligned pointers. out may be x or residual (dx may be dout) with
+ * equal strides. */
+int moe_dropout_forward(int dtype, int64_t rows, int64_t cols, const void* x, int64_t ldx,
+                        const void* residual, int64_t ldr, double p, const uint64_t* rng,
+                        void* out, int64_t ldo, void* stream);
+int moe_dropout_backward(int dtype, int64_t rows, int64_t cols, const void* dout,
+                         int64_t lddout, double p, const uint64_t* rng, void* dx,
+                         int64_t lddx, void* stream);
+
+/* Read (synchronously) and clear the status word of the operators above on the
+ * current device: MOE_OK, or MOE_DEVICE_TIMEOUT if a kernel abandoned a bounded
+ * wait since the last read (its outputs are invalid). */
+int moe_ops_device_status(void);
 
 #ifdef __cplusplus
 }

@@ -21,6 +21,9 @@ EXPORTED_SYMBOLS = [
     "moe_plan_device_status", "moe_plan_enable_timing", "moe_plan_kernel_times",
     "moe_plan_kernel_name", "moe_plan_last_launch_count", "moe_plan_destroy", "moe_strerror",
     "moe_last_error", "moe_forward_noalloc", "moe_plan_set_option", "moe_plan_capacity_seats",
+    "moe_norm_forward", "moe_norm_workspace_bytes", "moe_norm_backward",
+    "moe_gated_ffn_workspace_bytes", "moe_gated_ffn_forward", "moe_gated_ffn_backward",
+    "moe_dropout_forward", "moe_dropout_backward", "moe_ops_device_status",
 ]
 MOE_OPTION_PAIR_MIN_ROWS = 1
 MOE_OPTION_WIDE_TILES = 2
@@ -38,6 +41,10 @@ MOE_OPTION_DOWN_TILE_COLS = 13
 MOE_OPTION_GATHER_ROWS = 14
 MOE_OPTION_TEST_WAIT_TIMEOUT = 100
 
+MOE_DTYPE_BF16, MOE_DTYPE_FP16, MOE_DTYPE_FP32 = 0, 1, 2
+MOE_NORM_LAYER, MOE_NORM_RMS = 0, 1
+MOE_ACT_SILU, MOE_ACT_GELU = 0, 1
+
 STATUS_NAMES = {0: "MOE_OK", 1: "MOE_INVALID_CONFIG", 2: "MOE_INVALID_ARG",
                 3: "MOE_WORKSPACE_TOO_SMALL", 4: "MOE_CUDA_ERROR", 5: "MOE_UNSUPPORTED",
                 6: "MOE_DEVICE_TIMEOUT", 7: "MOE_DEVICE_INCONSISTENT"}
@@ -52,6 +59,7 @@ class MoEError(RuntimeError):
 _LIB: Optional[ctypes.CDLL] = None
 
 _vp, _i, _i64, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
+_dbl = ctypes.c_double
 
 
 def load_library(path: Optional[str] = None) -> ctypes.CDLL:
@@ -84,6 +92,20 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
         "moe_plan_destroy": (None, [_vp]),
         "moe_strerror": (ctypes.c_char_p, [_i]),
         "moe_last_error": (ctypes.c_char_p, []),
+        "moe_norm_forward": (_i, [_i, _i, _i, _i64, _i64, _vp, _i64, _vp, _vp, _dbl, _vp, _i64,
+                                  _vp, _vp, _vp]),
+        "moe_norm_workspace_bytes": (_sz, [_i, _i64, _i64]),
+        "moe_norm_backward": (_i, [_i, _i, _i, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp,
+                                   _vp, _i64, _vp, _vp, _vp, _sz, _vp]),
+        "moe_gated_ffn_workspace_bytes": (_sz, [_i64, _i64, _i64, _i]),
+        "moe_gated_ffn_forward": (_i, [_i, _i, _i64, _i64, _i64, _vp, _i64, _vp, _vp, _vp, _vp,
+                                       _i64, _vp, _vp, _vp, _sz, _vp]),
+        "moe_gated_ffn_backward": (_i, [_i, _i, _i64, _i64, _i64, _vp, _i64, _vp, _i64]
+                                   + [_vp] * 6 + [_i64] + [_vp] * 4 + [_sz, _vp]),
+        "moe_dropout_forward": (_i, [_i, _i64, _i64, _vp, _i64, _vp, _i64, _dbl, _vp, _vp, _i64,
+                                     _vp]),
+        "moe_dropout_backward": (_i, [_i, _i64, _i64, _vp, _i64, _dbl, _vp, _vp, _i64, _vp]),
+        "moe_ops_device_status": (_i, []),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)

@@ -17,14 +17,15 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIBDIR = os.path.join(PKG, "lib")
 LIBNAME = "libmoe_ffn.so"
-SOURCES = ["moe_ffn.cu"]
-HEADERS = ["ptx_sm100.cuh", "gemm_sm100.cuh", "route.cuh"]
+SOURCES = ["moe_ffn.cu", "gated_ffn.cu", "ops.cu"]
+HEADERS = ["ptx_sm100.cuh", "gemm_sm100.cuh", "route.cuh", "router_sm100.cuh",
+           "dense_gemm_sm100.cuh", "norm.cuh", "dropout.cuh", "ops_types.cuh", "ops_host.h"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-O3", "-lineinfo", "-std=c++17",
     "-Xcompiler", "-fPIC", "-shared",
-    "--expt-relaxed-constexpr",
+    "--expt-relaxed-constexpr", "--threads", "0",
 ]
 
 

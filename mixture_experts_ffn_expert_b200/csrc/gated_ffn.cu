@@ -1,0 +1,355 @@
+// gated_ffn.cu - C entry points of the gated feed-forward block with its backward pass
+// (declared in include/moe_ffn.h): argument checks, tensor maps, tile choice, launches.
+// Nothing here synchronises the host (moe_ops_device_status apart) or allocates device
+// memory.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <cstdint>
+#include <cstdio>
+
+#include "dense_gemm_sm100.cuh"
+#include "moe_ffn.h"
+#include "ops_host.h"
+
+namespace {
+
+using moe::launch_overlapped;
+using moe::set_error;
+
+// Set by a kernel that gave up a bounded wait; one word a device.
+__device__ int g_ops_status;
+
+constexpr int kMaxDevices = 64;
+
+struct DeviceInfo {
+  std::atomic<int> ready{0};
+  int sms = 0;
+  int* status = nullptr;
+};
+DeviceInfo g_devices[kMaxDevices];
+
+int cuda_error(cudaError_t e, const char* what) {
+  char buf[256];
+  snprintf(buf, sizeof(buf), "%s: %s", what, cudaGetErrorString(e));
+  cudaGetLastError();
+  return set_error(MOE_CUDA_ERROR, buf);
+}
+
+template <typename T, int EPI>
+cudaError_t set_smem() {
+  cudaError_t e = cudaFuncSetAttribute(moe::dense_gemm_kernel<T, EPI, true>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       int(moe::dense_smem_bytes<true>()));
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(moe::dense_gemm_kernel<T, EPI, false>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             int(moe::dense_smem_bytes<false>()));
+  return e;
+}
+
+// Properties of the current device; the first call on a device also raises the kernels'
+// shared-memory limits there (repeating that is harmless, so two first calls may race).
+int device_info(DeviceInfo** out) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_error(e, "no usable CUDA device");
+  if (dev >= kMaxDevices) return set_error(MOE_UNSUPPORTED, "device index above 63");
+  DeviceInfo& d = g_devices[dev];
+  if (!d.ready.load(std::memory_order_acquire)) {
+    int major = 0, minor = 0, sms = 0;
+    void* status = nullptr;
+    if ((e = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev)) ||
+        (e = cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev)) ||
+        (e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)))
+      return cuda_error(e, "device query");
+    if (major != 10 || minor != 0)
+      return set_error(MOE_UNSUPPORTED, "this library is built for sm_100a only");
+    if ((e = cudaGetSymbolAddress(&status, g_ops_status)) ||
+        (e = set_smem<__nv_bfloat16, moe::kGemmPlain>()) ||
+        (e = set_smem<__nv_bfloat16, moe::kGemmGluForward>()) ||
+        (e = set_smem<__nv_bfloat16, moe::kGemmGluBackward>()) ||
+        (e = set_smem<__half, moe::kGemmPlain>()) ||
+        (e = set_smem<__half, moe::kGemmGluForward>()) ||
+        (e = set_smem<__half, moe::kGemmGluBackward>()))
+      return cuda_error(e, "kernel attributes");
+    if (!moe::tensor_map_encoder())
+      return set_error(MOE_CUDA_ERROR, "cuTensorMapEncodeTiled is not available from the driver");
+    d.sms = sms;
+    d.status = static_cast<int*>(status);
+    d.ready.store(1, std::memory_order_release);
+  }
+  *out = &d;
+  return MOE_OK;
+}
+
+bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+size_t align_up(size_t v) { return (v + 255) / 256 * 256; }
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// One launch being put together: tensor maps and products.
+struct GemmLaunch {
+  moe::DenseMaps maps;
+  moe::DenseParams P = {};
+  int n_maps = 0;
+  int half;                 // 16-bit type: 1 fp16, 0 bf16
+  bool ok = true;
+
+  // Matrix (rows, cols), rows `ld` elements apart, in boxes of 64 columns x box_rows rows;
+  // what a box covers beyond the matrix reads as zero.
+  int map(const void* base, int64_t rows, int64_t cols, int64_t ld, int box_rows) {
+    cuuint64_t dims[2] = {cuuint64_t(cols), cuuint64_t(rows)};
+    cuuint64_t strides[1] = {cuuint64_t(ld) * 2};
+    cuuint32_t box[2] = {64, cuuint32_t(box_rows)};
+    cuuint32_t estr[2] = {1, 1};
+    ok = ok && moe::tensor_map_encoder()(
+                   &maps.m[n_maps],
+                   half ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                   const_cast<void*>(base), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return n_maps++;
+  }
+
+  void product(int M, int N, int tile_m, int tile_n, int64_t k0, int64_t k1, int a0, int a1,
+               int b0, int b1, int a_mn, int b_mn, void* out, int64_t ldo) {
+    moe::DenseProblem& q = P.p[P.n_problems++];
+    q.M = M;
+    q.N = N;
+    q.m_tiles = int(ceil_div(M, tile_m));
+    q.n_tiles = int(ceil_div(N, tile_n));
+    q.tile0 = P.total_tiles;
+    q.kb[0] = int(ceil_div(k0, 64));
+    q.kb[1] = int(ceil_div(k1, 64));
+    q.map_a[0] = a0;
+    q.map_a[1] = a1;
+    q.map_b[0] = b0;
+    q.map_b[1] = b1;
+    q.a_mn = a_mn;
+    q.b_mn = b_mn;
+    q.out = out;
+    q.ldo = ldo;
+    P.total_tiles += q.m_tiles * q.n_tiles;
+  }
+};
+
+template <typename T, int EPI, bool PAIR>
+cudaError_t launch(GemmLaunch& L, const DeviceInfo& d, cudaStream_t st) {
+  int workers = PAIR ? d.sms / 2 : d.sms;
+  if (workers > L.P.total_tiles) workers = L.P.total_tiles;
+  const moe::DenseProblem& q0 = L.P.p[0];
+  L.P.first_tiles = q0.m_tiles * q0.n_tiles;
+  L.P.extra = 0;
+  if (L.P.n_problems > 1) {
+    const int late = workers - L.P.first_tiles % workers;   // == workers: no remainder
+    const int rest = L.P.total_tiles - L.P.first_tiles;
+    const int k0 = q0.kb[0] + q0.kb[1], k1 = L.P.p[1].kb[0] + L.P.p[1].kb[1];
+    int extra = (k0 + k1 / 2) / k1;
+    if (late < workers && extra > rest / late) extra = rest / late;
+    if (late < workers) L.P.extra = extra;
+  }
+  L.P.status = d.status;
+  return launch_overlapped(moe::dense_gemm_kernel<T, EPI, PAIR>,
+                           dim3(PAIR ? 2 * workers : workers), dim3(moe::kDgThreads),
+                           moe::dense_smem_bytes<PAIR>(), st, PAIR ? 2 : 1, L.maps, L.P);
+}
+
+template <int EPI>
+cudaError_t launch_any(GemmLaunch& L, bool pair, const DeviceInfo& d, cudaStream_t st) {
+  if (L.half)
+    return pair ? launch<__half, EPI, true>(L, d, st) : launch<__half, EPI, false>(L, d, st);
+  return pair ? launch<__nv_bfloat16, EPI, true>(L, d, st)
+              : launch<__nv_bfloat16, EPI, false>(L, d, st);
+}
+
+// CTA pairs on 256 x 256 tiles once there are enough of them for every pair of SMs.
+bool use_pairs(int64_t m, int64_t n, int cols, const DeviceInfo& d) {
+  return ceil_div(m, 256) * ceil_div(n, cols) >= d.sms / 2;
+}
+
+int check_shape(int act, int dtype, int64_t T, int64_t d, int64_t f) {
+  if (act != MOE_ACT_SILU && act != MOE_ACT_GELU)
+    return set_error(MOE_INVALID_ARG, "activation must be MOE_ACT_SILU or MOE_ACT_GELU");
+  if (dtype != MOE_DTYPE_BF16 && dtype != MOE_DTYPE_FP16)
+    return set_error(MOE_INVALID_ARG, "the gated feed-forward block takes bf16 or fp16");
+  if (T < 0) return set_error(MOE_INVALID_ARG, "T must be >= 0");
+  if (d < 1 || f < 1) return set_error(MOE_INVALID_CONFIG, "d and f must be >= 1");
+  if (d % 8 || f % 8 || d > (1 << 20) || f > (1 << 20) || T > (1 << 24))
+    return set_error(MOE_UNSUPPORTED,
+                     "d and f must be multiples of 8 up to 2^20, T at most 2^24");
+  return MOE_OK;
+}
+
+int check_rows(const void* p, int64_t T, int64_t cols, int64_t ld, const char* what) {
+  char buf[128];
+  if (!p || !aligned(p, 16)) {
+    snprintf(buf, sizeof(buf), "%s must be non-null and 16-byte aligned", what);
+    return set_error(MOE_INVALID_ARG, buf);
+  }
+  if (T > 1 && (ld < cols || ld % 8 || ld > (1LL << 31))) {
+    snprintf(buf, sizeof(buf), "%s: the row stride must be a multiple of 8 and >= its width",
+             what);
+    return set_error(MOE_INVALID_ARG, buf);
+  }
+  return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t moe_gated_ffn_workspace_bytes(int64_t T, int64_t d, int64_t f, int backward) {
+  if (check_shape(MOE_ACT_SILU, MOE_DTYPE_BF16, T, d, f) != MOE_OK) return 0;
+  return (backward ? 3 : 1) * align_up(size_t(T) * f * 2);
+}
+
+int moe_gated_ffn_forward(int act, int dtype, int64_t T, int64_t d, int64_t f, const void* x,
+                          int64_t ldx, const void* W1, const void* W3, const void* W2, void* out,
+                          int64_t ldo, void* gate, void* up, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+  if (int s = check_shape(act, dtype, T, d, f)) return s;
+  if (T == 0) return MOE_OK;
+  if (int s = check_rows(x, T, d, ldx, "x")) return s;
+  if (int s = check_rows(out, T, d, ldo, "out")) return s;
+  if (int s = check_rows(W1, 1, d, d, "W1")) return s;
+  if (int s = check_rows(W3, 1, d, d, "W3")) return s;
+  if (int s = check_rows(W2, 1, f, f, "W2")) return s;
+  if ((gate == nullptr) != (up == nullptr) || !aligned(gate, 16) || !aligned(up, 16))
+    return set_error(MOE_INVALID_ARG, "gate and up must be both null or both 16-byte aligned");
+  if (workspace_bytes < moe_gated_ffn_workspace_bytes(T, d, f, 0))
+    return set_error(MOE_WORKSPACE_TOO_SMALL, "gated feed-forward: workspace too small");
+  if (!workspace || !aligned(workspace, 256))
+    return set_error(MOE_INVALID_ARG, "workspace must be non-null and 256-byte aligned");
+  if (T == 1) ldx = ldo = d;
+  DeviceInfo* dev;
+  if (int s = device_info(&dev)) return s;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int m = int(T);
+  {
+    GemmLaunch L;
+    L.half = dtype == MOE_DTYPE_FP16;
+    const bool pair = use_pairs(T, f, 128, *dev);
+    const int a = L.map(x, T, d, ldx, 128);
+    const int b1 = L.map(W1, f, d, d, pair ? 128 : 64);
+    const int b3 = L.map(W3, f, d, d, pair ? 128 : 64);
+    if (!L.ok) return set_error(MOE_CUDA_ERROR, "tensor map encoding failed");
+    L.product(m, int(f), pair ? 256 : 128, pair ? 128 : 64, d, 0, a, a, b1, b3, 0, 0, nullptr, 0);
+    L.P.hidden = workspace;
+    L.P.gate = gate;
+    L.P.up = up;
+    L.P.act = act;
+    const cudaError_t e = launch_any<moe::kGemmGluForward>(L, pair, *dev, st);
+    if (e != cudaSuccess) return cuda_error(e, "gated feed-forward gate/up launch");
+  }
+  GemmLaunch L;
+  L.half = dtype == MOE_DTYPE_FP16;
+  const bool pair = use_pairs(T, d, 256, *dev);
+  const int a = L.map(workspace, T, f, f, 128);
+  const int b = L.map(W2, d, f, f, 128);
+  if (!L.ok) return set_error(MOE_CUDA_ERROR, "tensor map encoding failed");
+  const int tile = pair ? 256 : 128;
+  L.product(m, int(d), tile, tile, f, 0, a, a, b, b, 0, 0, out, ldo);
+  const cudaError_t e = launch_any<moe::kGemmPlain>(L, pair, *dev, st);
+  if (e != cudaSuccess) return cuda_error(e, "gated feed-forward down launch");
+  return MOE_OK;
+}
+
+int moe_gated_ffn_backward(int act, int dtype, int64_t T, int64_t d, int64_t f, const void* dout,
+                           int64_t lddout, const void* x, int64_t ldx, const void* W1,
+                           const void* W3, const void* W2, const void* gate, const void* up,
+                           void* dx, int64_t lddx, void* dW1, void* dW3, void* dW2,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+  if (int s = check_shape(act, dtype, T, d, f)) return s;
+  if (!dx && !dW1 && !dW3 && !dW2) return MOE_OK;
+  if (!aligned(dW1, 16) || !aligned(dW3, 16) || !aligned(dW2, 16))
+    return set_error(MOE_INVALID_ARG, "dW1, dW3 and dW2 must be 16-byte aligned");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (T == 0) {                        // sums over no tokens
+    void* grads[3] = {dW1, dW3, dW2};
+    for (void* g : grads)
+      if (g) {
+        const cudaError_t e = cudaMemsetAsync(g, 0, size_t(d) * f * 2, st);
+        if (e != cudaSuccess) return cuda_error(e, "gated feed-forward backward");
+      }
+    return MOE_OK;
+  }
+  if (int s = check_rows(dout, T, d, lddout, "dout")) return s;
+  if (int s = check_rows(x, T, d, ldx, "x")) return s;
+  if (dx)
+    if (int s = check_rows(dx, T, d, lddx, "dx")) return s;
+  if (int s = check_rows(W1, 1, d, d, "W1")) return s;
+  if (int s = check_rows(W3, 1, d, d, "W3")) return s;
+  if (int s = check_rows(W2, 1, f, f, "W2")) return s;
+  if (int s = check_rows(gate, 1, f, f, "gate")) return s;
+  if (int s = check_rows(up, 1, f, f, "up")) return s;
+  if (workspace_bytes < moe_gated_ffn_workspace_bytes(T, d, f, 1))
+    return set_error(MOE_WORKSPACE_TOO_SMALL, "gated feed-forward backward: workspace too small");
+  if (!workspace || !aligned(workspace, 256))
+    return set_error(MOE_INVALID_ARG, "workspace must be non-null and 256-byte aligned");
+  if (T == 1) ldx = lddx = lddout = d;
+  DeviceInfo* dev;
+  if (int s = device_info(&dev)) return s;
+  const size_t plane = align_up(size_t(T) * f * 2);
+  char* ws = static_cast<char*>(workspace);
+  void *dgate = ws, *dup = ws + plane, *hidden = ws + 2 * plane;
+  const int m = int(T);
+  {
+    GemmLaunch L;
+    L.half = dtype == MOE_DTYPE_FP16;
+    const bool pair = use_pairs(T, f, 256, *dev);
+    const int a = L.map(dout, T, d, lddout, 128);
+    const int b = L.map(W2, d, f, f, 64);
+    if (!L.ok) return set_error(MOE_CUDA_ERROR, "tensor map encoding failed");
+    const int tile = pair ? 256 : 128;
+    L.product(m, int(f), tile, tile, d, 0, a, a, b, b, 0, 1, nullptr, 0);
+    L.P.gate = const_cast<void*>(gate);
+    L.P.up = const_cast<void*>(up);
+    L.P.dgate = dgate;
+    L.P.dup = dup;
+    L.P.hidden = hidden;
+    L.P.act = act;
+    const cudaError_t e = launch_any<moe::kGemmGluBackward>(L, pair, *dev, st);
+    if (e != cudaSuccess) return cuda_error(e, "gated feed-forward dh launch");
+  }
+  GemmLaunch L;
+  L.half = dtype == MOE_DTYPE_FP16;
+  const bool pair = use_pairs(f, d, 256, *dev);
+  const int tile = pair ? 256 : 128;
+  if (dx) {
+    const int a0 = L.map(dgate, T, f, f, 128), a1 = L.map(dup, T, f, f, 128);
+    const int b0 = L.map(W1, f, d, d, 64), b1 = L.map(W3, f, d, d, 64);
+    L.product(m, int(d), tile, tile, f, f, a0, a1, b0, b1, 0, 1, dx, lddx);
+  }
+  const int xm = dW1 || dW3 ? L.map(x, T, d, ldx, 64) : 0;
+  if (dW1) {
+    const int a = L.map(dgate, T, f, f, 64);
+    L.product(int(f), int(d), tile, tile, T, 0, a, a, xm, xm, 1, 1, dW1, d);
+  }
+  if (dW3) {
+    const int a = L.map(dup, T, f, f, 64);
+    L.product(int(f), int(d), tile, tile, T, 0, a, a, xm, xm, 1, 1, dW3, d);
+  }
+  if (dW2) {
+    const int a = L.map(dout, T, d, lddout, 64), b = L.map(hidden, T, f, f, 64);
+    L.product(int(d), int(f), tile, tile, T, 0, a, a, b, b, 1, 1, dW2, f);
+  }
+  if (!L.ok) return set_error(MOE_CUDA_ERROR, "tensor map encoding failed");
+  const cudaError_t e = launch_any<moe::kGemmPlain>(L, pair, *dev, st);
+  if (e != cudaSuccess) return cuda_error(e, "gated feed-forward gradient launch");
+  return MOE_OK;
+}
+
+int moe_ops_device_status(void) {
+  DeviceInfo* dev;
+  if (int s = device_info(&dev)) return s;
+  int v = 0;
+  cudaError_t e = cudaMemcpy(&v, dev->status, sizeof(int), cudaMemcpyDeviceToHost);
+  if (e == cudaSuccess && v != 0) e = cudaMemset(dev->status, 0, sizeof(int));
+  if (e != cudaSuccess) return cuda_error(e, "device status read");
+  if (v != MOE_OK) return set_error(v, "an operator's kernel gave up a bounded wait");
+  return MOE_OK;
+}
+
+}  // extern "C"

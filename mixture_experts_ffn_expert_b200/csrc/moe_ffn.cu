@@ -17,6 +17,7 @@
 
 #include "moe_ffn.h"
 #include "gemm_sm100.cuh"
+#include "ops_host.h"
 #include "route.cuh"
 #include "router_sm100.cuh"
 
@@ -282,10 +283,7 @@ Layout make_layout(const moe_plan* p, int64_t T) {
 }
 
 // ------------------------------------------------------------- tensor maps
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+using moe::EncodeTiledFn;
 
 EncodeTiledFn encode_fn() {
   static EncodeTiledFn fn = nullptr;
@@ -634,6 +632,11 @@ int noalloc_scratch_address(void** out) {
 }
 
 }  // namespace
+
+namespace moe {
+int set_error(int status, const char* message) { return fail(status, "%s", message); }
+EncodeTiledFn tensor_map_encoder() { return encode_fn(); }
+}  // namespace moe
 
 extern "C" {
 

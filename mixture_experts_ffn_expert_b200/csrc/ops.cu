@@ -1,0 +1,360 @@
+// ops.cu - C entry points of the norm and dropout operators (declared in
+// include/moe_ffn.h): argument checks, kernel choice and launch. Nothing here
+// synchronises the host or allocates device memory.
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <cstdio>
+
+#include "dropout.cuh"
+#include "moe_ffn.h"
+#include "norm.cuh"
+#include "ops_host.h"
+
+namespace {
+
+using moe::launch_overlapped;
+using moe::set_error;
+
+int dtype_size(int dtype) {
+  return dtype == MOE_DTYPE_FP32 ? 4 : dtype == MOE_DTYPE_BF16 || dtype == MOE_DTYPE_FP16 ? 2 : 0;
+}
+
+bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+int launch_status(cudaError_t e, const char* what) {
+  if (e == cudaSuccess) e = cudaGetLastError();
+  if (e == cudaSuccess) return MOE_OK;
+  char buf[256];
+  snprintf(buf, sizeof(buf), "%s launch failed: %s", what, cudaGetErrorString(e));
+  cudaGetLastError();
+  return set_error(MOE_CUDA_ERROR, buf);
+}
+
+// Shape and stride checks shared by the row operators; null when they pass.
+const char* check_rows(int64_t rows, int64_t cols) {
+  if (rows < 0) return "rows must be >= 0";
+  if (cols < 1) return "cols must be >= 1";
+  return nullptr;
+}
+bool bad_stride(int64_t rows, int64_t cols, int64_t ld) { return rows > 1 && ld < cols; }
+
+constexpr int64_t kMaxRows = (1LL << 31) - 1;
+constexpr int64_t kMaxCols = 1LL << 24;
+
+// ------------------------------------------------------------------ norm
+constexpr int kNormBlocks = 296;        // blocks (partial rows) of a backward pass, two an SM
+
+int round32(int64_t v) { return static_cast<int>((v + 31) / 32 * 32); }
+
+template <typename T, int VEC, int VPT>
+cudaError_t launch_norm_forward(const moe::NormParams& P, int group, cudaStream_t st) {
+  const int per_block = group == 32 ? 4 : 1;
+  const int64_t blocks = (P.rows + per_block - 1) / per_block;
+  return launch_overlapped(moe::norm_forward_kernel<T, VEC, VPT>, dim3(unsigned(blocks)),
+                           dim3(group * per_block), 0, st, 1, P, group);
+}
+
+template <typename T>
+cudaError_t norm_forward_any(const moe::NormParams& P, bool vec, cudaStream_t st) {
+  constexpr int V = 16 / sizeof(T);
+  // Few rows: as many threads a row as it has vectors (latency). Many rows: several
+  // vectors a thread, short rows a warp each (no block barrier in the statistics).
+  const bool few = P.rows < 592;
+  if (vec) {
+    const int n = P.cols / V;
+    if (n <= 32) return launch_norm_forward<T, V, 1>(P, 32, st);
+    if (!few && n <= 64) return launch_norm_forward<T, V, 2>(P, 32, st);
+    if (!few && n <= 128) return launch_norm_forward<T, V, 4>(P, 32, st);
+    if (!few && n <= 256) return launch_norm_forward<T, V, 8>(P, 32, st);
+    if (few && n <= 1024) return launch_norm_forward<T, V, 1>(P, round32(n), st);
+    if (n <= 2048) return launch_norm_forward<T, V, 4>(P, round32((n + 3) / 4), st);
+    if (n <= 8192) return launch_norm_forward<T, V, 8>(P, round32((n + 7) / 8), st);
+  } else {
+    if (P.cols <= 32) return launch_norm_forward<T, 1, 1>(P, 32, st);
+    if (!few && P.cols <= 128) return launch_norm_forward<T, 1, 4>(P, 32, st);
+    if (!few && P.cols <= 512) return launch_norm_forward<T, 1, 16>(P, 32, st);
+    if (P.cols <= 4096) return launch_norm_forward<T, 1, 4>(P, round32((P.cols + 3) / 4), st);
+    if (P.cols <= 16384)
+      return launch_norm_forward<T, 1, 16>(P, round32((P.cols + 15) / 16), st);
+  }
+  const int64_t blocks = P.rows < 592 ? P.rows : 592;
+  return launch_overlapped(moe::norm_forward_long_kernel<T>, dim3(unsigned(blocks)), dim3(1024), 0,
+                           st, 1, P);
+}
+
+template <typename T, int VEC, int VPT, bool RMS, bool GRADW>
+cudaError_t launch_norm_backward(const moe::NormParams& P, int group, int* blocks,
+                                 cudaStream_t st) {
+  int groups = 512 / group;
+  if (groups < 1) groups = 1;
+  if (groups > 8) groups = 8;
+  const size_t smem = groups > 1 ? size_t(RMS ? 1 : 2) * P.cols * sizeof(float) : 0;
+  int64_t n = (P.rows + groups - 1) / groups;
+  const int cap = group * groups > 512 ? kNormBlocks / 2 : kNormBlocks;
+  if (n > cap) n = cap;
+  *blocks = static_cast<int>(n);
+  return launch_overlapped(moe::norm_backward_kernel<T, VEC, VPT, RMS, GRADW>, dim3(unsigned(n)),
+                           dim3(group * groups), smem, st, 1, P, group);
+}
+
+template <typename T, bool RMS, bool GRADW>
+cudaError_t norm_backward_any(const moe::NormParams& P, bool vec, int* blocks, cudaStream_t st) {
+  constexpr int V = 16 / sizeof(T);
+  if (vec) {
+    const int n = P.cols / V;
+    if (n <= 1024) return launch_norm_backward<T, V, 1, RMS, GRADW>(P, round32(n), blocks, st);
+    if (n <= 2048)
+      return launch_norm_backward<T, V, 2, RMS, GRADW>(P, round32((n + 1) / 2), blocks, st);
+    if (n <= 4096)
+      return launch_norm_backward<T, V, 4, RMS, GRADW>(P, round32((n + 3) / 4), blocks, st);
+  } else {
+    if (P.cols <= 4096)
+      return launch_norm_backward<T, 1, 4, RMS, GRADW>(P, round32((P.cols + 3) / 4), blocks, st);
+    if (P.cols <= 16384)
+      return launch_norm_backward<T, 1, 16, RMS, GRADW>(P, round32((P.cols + 15) / 16), blocks,
+                                                        st);
+  }
+  cudaError_t e = cudaSuccess;
+  if (GRADW) {                          // before dx, which may overwrite dy
+    *blocks = static_cast<int>(P.rows < 32 ? P.rows : 32);
+    e = launch_overlapped(moe::norm_backward_long_sum_kernel<T>,
+                          dim3(unsigned((P.cols + 255) / 256), *blocks), dim3(256), 0, st, 1, P);
+  }
+  if (P.y && e == cudaSuccess) {
+    const int64_t n = P.rows < 592 ? P.rows : 592;
+    e = launch_overlapped(moe::norm_backward_long_kernel<T>, dim3(unsigned(n)), dim3(1024), 0, st,
+                          1, P);
+  }
+  return e;
+}
+
+template <typename T>
+cudaError_t norm_backward_typed(const moe::NormParams& P, bool vec, bool gradw, int* blocks,
+                                cudaStream_t st) {
+  if (P.rms)
+    return gradw ? norm_backward_any<T, true, true>(P, vec, blocks, st)
+                 : norm_backward_any<T, true, false>(P, vec, blocks, st);
+  return gradw ? norm_backward_any<T, false, true>(P, vec, blocks, st)
+               : norm_backward_any<T, false, false>(P, vec, blocks, st);
+}
+
+// Whether rows of this tensor can be read as 16-byte vectors.
+bool vector_rows(const void* p, int64_t rows, int64_t ld, int esize) {
+  return aligned(p, 16) && (rows <= 1 || (ld * esize) % 16 == 0);
+}
+
+int check_norm(int kind, int dtype, int wdtype, int64_t rows, int64_t cols) {
+  if (kind != MOE_NORM_LAYER && kind != MOE_NORM_RMS)
+    return set_error(MOE_INVALID_ARG, "kind must be MOE_NORM_LAYER or MOE_NORM_RMS");
+  if (!dtype_size(dtype)) return set_error(MOE_INVALID_ARG, "unknown dtype");
+  if (wdtype != dtype && wdtype != MOE_DTYPE_FP32)
+    return set_error(MOE_INVALID_ARG, "weights must have x's dtype or fp32");
+  if (const char* m = check_rows(rows, cols)) return set_error(MOE_INVALID_ARG, m);
+  if (rows > kMaxRows || cols > kMaxCols)
+    return set_error(MOE_UNSUPPORTED, "norm needs rows < 2^31 and cols <= 2^24");
+  return MOE_OK;
+}
+
+// ------------------------------------------------------------------ dropout
+template <typename T, bool RES>
+cudaError_t launch_dropout(const moe::DropoutParams& P, bool flat, cudaStream_t st) {
+  const int64_t per_thread = flat ? 16 / sizeof(T) : 4;
+  int64_t blocks = (P.n / per_thread + 255) / 256;
+  if (blocks < 1) blocks = 1;
+  if (blocks > (1 << 20)) blocks = 1 << 20;      // the rest of a larger tensor by stride
+  if (flat)
+    return launch_overlapped(moe::dropout_flat_kernel<T, RES>, dim3(unsigned(blocks)), dim3(256),
+                             0, st, 1, P);
+  return launch_overlapped(moe::dropout_strided_kernel<T, RES>, dim3(unsigned(blocks)), dim3(256),
+                           0, st, 1, P);
+}
+
+int dropout_run(int dtype, int64_t rows, int64_t cols, const void* x, int64_t ldx,
+                const void* residual, int64_t ldr, double p, const uint64_t* rng, void* out,
+                int64_t ldo, void* stream) {
+  const int es = dtype_size(dtype);
+  if (!es) return set_error(MOE_INVALID_ARG, "unknown dtype");
+  if (const char* m = check_rows(rows, cols)) return set_error(MOE_INVALID_ARG, m);
+  if (!(p >= 0.0 && p <= 1.0)) return set_error(MOE_INVALID_ARG, "p must lie in [0, 1]");
+  if (rows > (1LL << 40) || cols > (1LL << 40) || (rows > 0 && cols > (1LL << 45) / rows))
+    return set_error(MOE_UNSUPPORTED, "dropout needs at most 2^45 elements");
+  if (rows == 0) return MOE_OK;
+  if (!x || !out) return set_error(MOE_INVALID_ARG, "input and output must be non-null");
+  if (bad_stride(rows, cols, ldx) || bad_stride(rows, cols, ldo) ||
+      (residual && bad_stride(rows, cols, ldr)))
+    return set_error(MOE_INVALID_ARG, "a row stride is smaller than cols");
+  if (!aligned(x, es) || !aligned(out, es) || (residual && !aligned(residual, es)))
+    return set_error(MOE_INVALID_ARG, "a tensor is not aligned to its elements");
+  if (rows == 1) ldx = ldo = ldr = cols;
+  moe::DropoutParams P = {};
+  P.x = x;
+  P.residual = residual;
+  P.out = out;
+  P.n = rows * cols;
+  P.cols = cols;
+  P.ldx = ldx;
+  P.ldr = ldr;
+  P.ldo = ldo;
+  P.rng = reinterpret_cast<const unsigned long long*>(rng);
+  const double t = std::nearbyint(p * 4294967296.0);
+  P.mode = t >= 4294967296.0 ? 2 : t > 0.0 ? 1 : 0;
+  P.threshold = P.mode == 1 ? static_cast<uint32_t>(t) : 0u;
+  P.scale = p < 1.0 ? static_cast<float>(1.0 / (1.0 - p)) : 0.0f;
+  if (P.mode == 1 && (!rng || !aligned(rng, 8)))
+    return set_error(MOE_INVALID_ARG, "rng must point to two uint64 on the device when p > 0");
+  const bool flat = ldx == cols && ldo == cols && (!residual || ldr == cols) && aligned(x, 16) &&
+                    aligned(out, 16) && (!residual || aligned(residual, 16));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (dtype == MOE_DTYPE_BF16)
+    e = residual ? launch_dropout<__nv_bfloat16, true>(P, flat, st)
+                 : launch_dropout<__nv_bfloat16, false>(P, flat, st);
+  else if (dtype == MOE_DTYPE_FP16)
+    e = residual ? launch_dropout<__half, true>(P, flat, st)
+                 : launch_dropout<__half, false>(P, flat, st);
+  else
+    e = residual ? launch_dropout<float, true>(P, flat, st)
+                 : launch_dropout<float, false>(P, flat, st);
+  return launch_status(e, "dropout");
+}
+
+}  // namespace
+
+extern "C" {
+
+int moe_norm_forward(int kind, int dtype, int wdtype, int64_t rows, int64_t cols, const void* x,
+                     int64_t ldx, const void* weight, const void* bias, double eps, void* y,
+                     int64_t ldy, float* mean, float* rstd, void* stream) {
+  if (int s = check_norm(kind, dtype, wdtype, rows, cols)) return s;
+  if (!(eps >= 0.0) || !std::isfinite(eps))
+    return set_error(MOE_INVALID_ARG, "eps must be finite and >= 0");
+  if (kind == MOE_NORM_RMS && (bias || mean))
+    return set_error(MOE_INVALID_ARG, "an RMS norm has no bias and no mean");
+  if (rows == 0) return MOE_OK;
+  if (!x || !y) return set_error(MOE_INVALID_ARG, "x and y must be non-null");
+  if (bad_stride(rows, cols, ldx) || bad_stride(rows, cols, ldy))
+    return set_error(MOE_INVALID_ARG, "a row stride is smaller than cols");
+  const int es = dtype_size(dtype), ws = dtype_size(wdtype);
+  if (!aligned(x, es) || !aligned(y, es) || !aligned(weight, ws) || !aligned(bias, ws) ||
+      !aligned(mean, 4) || !aligned(rstd, 4))
+    return set_error(MOE_INVALID_ARG, "a tensor is not aligned to its elements");
+  moe::NormParams P = {};
+  P.x = x;
+  P.weight = weight;
+  P.bias = bias;
+  P.y = y;
+  P.mean = mean;
+  P.rstd = rstd;
+  P.rows = rows;
+  P.ldx = ldx;
+  P.ldy = ldy;
+  P.cols = static_cast<int>(cols);
+  P.eps = static_cast<float>(eps);
+  P.rms = kind == MOE_NORM_RMS;
+  P.wf32 = wdtype == MOE_DTYPE_FP32;
+  const bool vec = cols % (16 / es) == 0 && vector_rows(x, rows, ldx, es) &&
+                   vector_rows(y, rows, ldy, es) && aligned(weight, 16) && aligned(bias, 16);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = dtype == MOE_DTYPE_BF16   ? norm_forward_any<__nv_bfloat16>(P, vec, st)
+                        : dtype == MOE_DTYPE_FP16 ? norm_forward_any<__half>(P, vec, st)
+                                                  : norm_forward_any<float>(P, vec, st);
+  return launch_status(e, "norm forward");
+}
+
+size_t moe_norm_workspace_bytes(int kind, int64_t rows, int64_t cols) {
+  if (check_norm(kind, MOE_DTYPE_FP32, MOE_DTYPE_FP32, rows, cols) != MOE_OK) return 0;
+  const int64_t blocks = rows < kNormBlocks ? rows : kNormBlocks;
+  return size_t(blocks) * (kind == MOE_NORM_RMS ? 1 : 2) * size_t(cols) * sizeof(float);
+}
+
+int moe_norm_backward(int kind, int dtype, int wdtype, int64_t rows, int64_t cols, const void* dy,
+                      int64_t lddy, const void* x, int64_t ldx, const void* weight,
+                      const float* mean, const float* rstd, void* dx, int64_t lddx, void* dweight,
+                      void* dbias, void* workspace, size_t workspace_bytes, void* stream) {
+  if (int s = check_norm(kind, dtype, wdtype, rows, cols)) return s;
+  if (kind == MOE_NORM_RMS && (dbias || mean))
+    return set_error(MOE_INVALID_ARG, "an RMS norm has no bias and no mean");
+  if (!dx && !dweight && !dbias) return MOE_OK;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int es = dtype_size(dtype), ws = dtype_size(wdtype);
+  if (!aligned(dweight, ws) || !aligned(dbias, ws))
+    return set_error(MOE_INVALID_ARG, "a tensor is not aligned to its elements");
+  if (rows == 0) {                     // sums over no rows
+    cudaError_t e = cudaSuccess;
+    if (dweight) e = cudaMemsetAsync(dweight, 0, size_t(cols) * ws, st);
+    if (dbias && e == cudaSuccess) e = cudaMemsetAsync(dbias, 0, size_t(cols) * ws, st);
+    return launch_status(e, "norm backward");
+  }
+  if (!dy || !x || !rstd || (kind == MOE_NORM_LAYER && !mean))
+    return set_error(MOE_INVALID_ARG, "dy, x, rstd and (layer norm) mean must be non-null");
+  if (bad_stride(rows, cols, lddy) || bad_stride(rows, cols, ldx) ||
+      (dx && bad_stride(rows, cols, lddx)))
+    return set_error(MOE_INVALID_ARG, "a row stride is smaller than cols");
+  if (!aligned(dy, es) || !aligned(x, es) || !aligned(dx, es) || !aligned(weight, ws) ||
+      !aligned(mean, 4) || !aligned(rstd, 4))
+    return set_error(MOE_INVALID_ARG, "a tensor is not aligned to its elements");
+  const bool gradw = dweight || dbias;
+  if (gradw) {
+    if (workspace_bytes < moe_norm_workspace_bytes(kind, rows, cols))
+      return set_error(MOE_WORKSPACE_TOO_SMALL, "norm backward: workspace too small");
+    if (!workspace || !aligned(workspace, 16))
+      return set_error(MOE_INVALID_ARG, "workspace must be non-null and 16-byte aligned");
+  }
+  moe::NormParams P = {};
+  P.x = x;
+  P.dy = dy;
+  P.weight = weight;
+  P.y = dx;
+  P.mean = const_cast<float*>(mean);
+  P.rstd = const_cast<float*>(rstd);
+  P.partial = static_cast<float*>(workspace);
+  P.rows = rows;
+  P.ldx = ldx;
+  P.lddy = lddy;
+  P.ldy = lddx;
+  P.cols = static_cast<int>(cols);
+  P.rms = kind == MOE_NORM_RMS;
+  P.wf32 = wdtype == MOE_DTYPE_FP32;
+  const bool vec = cols % (16 / es) == 0 && vector_rows(x, rows, ldx, es) &&
+                   vector_rows(dy, rows, lddy, es) && (!dx || vector_rows(dx, rows, lddx, es)) &&
+                   aligned(weight, 16);
+  int blocks = 0;
+  cudaError_t e = dtype == MOE_DTYPE_BF16
+                      ? norm_backward_typed<__nv_bfloat16>(P, vec, gradw, &blocks, st)
+                  : dtype == MOE_DTYPE_FP16
+                      ? norm_backward_typed<__half>(P, vec, gradw, &blocks, st)
+                      : norm_backward_typed<float>(P, vec, gradw, &blocks, st);
+  if (e == cudaSuccess && gradw) {
+    const dim3 grid(unsigned((cols + 31) / 32), dbias ? 2 : 1);
+    const int planes = P.rms ? 1 : 2;
+    if (wdtype == MOE_DTYPE_FP32)
+      e = launch_overlapped(moe::norm_reduce_kernel<float>, grid, dim3(512), 0, st, 1,
+                            P.partial, blocks, planes, P.cols, static_cast<float*>(dweight),
+                            static_cast<float*>(dbias));
+    else if (wdtype == MOE_DTYPE_BF16)
+      e = launch_overlapped(moe::norm_reduce_kernel<__nv_bfloat16>, grid, dim3(512), 0, st, 1,
+                            P.partial, blocks, planes, P.cols,
+                            static_cast<__nv_bfloat16*>(dweight),
+                            static_cast<__nv_bfloat16*>(dbias));
+    else
+      e = launch_overlapped(moe::norm_reduce_kernel<__half>, grid, dim3(512), 0, st, 1, P.partial,
+                            blocks, planes, P.cols, static_cast<__half*>(dweight),
+                            static_cast<__half*>(dbias));
+  }
+  return launch_status(e, "norm backward");
+}
+
+int moe_dropout_forward(int dtype, int64_t rows, int64_t cols, const void* x, int64_t ldx,
+                        const void* residual, int64_t ldr, double p, const uint64_t* rng,
+                        void* out, int64_t ldo, void* stream) {
+  return dropout_run(dtype, rows, cols, x, ldx, residual, ldr, p, rng, out, ldo, stream);
+}
+
+int moe_dropout_backward(int dtype, int64_t rows, int64_t cols, const void* dout, int64_t lddout,
+                         double p, const uint64_t* rng, void* dx, int64_t lddx, void* stream) {
+  return dropout_run(dtype, rows, cols, dout, lddout, nullptr, 0, p, rng, dx, lddx, stream);
+}
+
+}  // extern "C"

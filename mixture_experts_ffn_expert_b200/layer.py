@@ -17,6 +17,7 @@ from .binding import (MOE_OPTION_BIAS_SELECTION_ONLY, MOE_OPTION_CAPACITY_FACTOR
                       MOE_OPTION_INTERLEAVE, MOE_OPTION_SHARED_CONCURRENT,
                       MOE_OPTION_SWIGLU_TILE_COLS, MOE_OPTION_TILE_ROWS, MOE_OPTION_WIDE_TILES,
                       MoEError, Plan)
+from .ops import dropout_add_forward, norm_forward
 
 __all__ = ["MoELayer", "MoEError"]
 
@@ -143,6 +144,19 @@ class MoELayer:
         return out
 
     __call__ = forward
+
+    def block(self, x: torch.Tensor, norm_weight: Optional[torch.Tensor] = None,
+              norm_bias: Optional[torch.Tensor] = None, norm: str = "rms", eps: float = 1e-5,
+              p: float = 0.0, rng: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """The block around the layer: x + dropout(forward(norm(x))), bf16 (T, d).
+
+        ``norm`` is "rms" or "layer"; p = 0 (inference) adds the plain residual, p > 0 draws
+        the dropout mask from ``rng`` (see ``ops.dropout_add_forward``). "Shared Expert
+        (DeepSeek-V3)", "How it works": the layer's input is normalised, the residual is
+        added at block level.
+        """
+        h = norm_forward(x, norm_weight, norm_bias, eps, norm)
+        return dropout_add_forward(self.forward(h), x, p, rng)
 
     def routing(self) -> Dict[str, torch.Tensor]:
         """idx, w, counts, offsets, perm_src, inv_pos of the last forward (device tensors)."""
