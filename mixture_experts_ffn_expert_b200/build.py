@@ -19,7 +19,7 @@ LIBDIR = os.path.join(PKG, "lib")
 LIBNAME = "libmoe_ffn.so"
 SOURCES = ["moe_ffn.cu", "gated_ffn.cu", "ops.cu"]
 HEADERS = ["ptx_sm100.cuh", "gemm_sm100.cuh", "route.cuh", "router_sm100.cuh",
-           "dense_gemm_sm100.cuh", "norm.cuh", "dropout.cuh", "ops_types.cuh", "ops_host.h"]
+           "dense_gemm_sm100.cuh", "stream_gemm_sm100.cuh", "norm.cuh", "dropout.cuh", "ops_types.cuh", "ops_host.h"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

@@ -33,10 +33,27 @@ enum { kActSilu = 0, kActGelu = 1 };
 
 constexpr int kDgThreads = 224;
 constexpr int kDgMaxProblems = 4;
-constexpr int kDgMaxMaps = 10;
+constexpr int kDgMaxMaps = 14;
 constexpr int kDgTileBytes = 16384;                 // one operand's 128 x 64 stage
 constexpr int kDgStageBytes = 2 * kDgTileBytes;
-constexpr int kDgStages = 6;
+
+// Outputs leave through shared memory: the epilogue warps write a chunk of their tile
+// there (swizzled, so that a thread's row does not collide with its neighbours') and one
+// thread stores it with TMA, which writes whole lines and clips what lies outside the
+// matrix. (Stored from registers, a warp's 16-byte stores went to 32 different rows; the
+// dh product of a 4096 x 4096 x 14336 step, which reads two and writes three matrices in
+// its epilogue, took 490 us that way.) Plain products use chunks of 64 columns, those
+// with three outputs 32, double-buffered either way.
+template <int EPI>
+struct DenseCfg {
+  static constexpr int kChunk = EPI == 0 ? 64 : 32;
+  static constexpr int kOuts = EPI == 0 ? 1 : 3;
+  static constexpr int kStages = EPI == 0 ? 6 : 5;
+  static constexpr int kBufBytes = 128 * kChunk * 2;
+  static constexpr int kSetBytes = kOuts * kBufBytes;
+  static constexpr size_t kSmem =
+      1024 + size_t(kStages) * kDgStageBytes + 2 * size_t(kSetBytes) + 256;
+};
 
 struct DenseProblem {
   int m_tiles, n_tiles, tile0;      // tile0: tiles of the problems before it
@@ -44,8 +61,7 @@ struct DenseProblem {
   int kb[2];                        // k-blocks of 64 in the two segments of the reduction
   int map_a[2], map_b[2];           // tensor maps of the segments
   int a_mn, b_mn;                   // 1: m (n) is the contiguous dimension
-  void* out;
-  long long ldo;
+  int map_out[3];                   // plain: D; gate/up: h, gate, up; dh: h, dgate, dup
 };
 
 struct DenseParams {
@@ -53,8 +69,8 @@ struct DenseParams {
   int n_problems, total_tiles;
   int first_tiles;                  // tiles of problem 0 (the costly ones)
   int extra;                        // see tile_of
-  // gate / up epilogues
-  void *gate, *up, *hidden, *dgate, *dup;
+  const void *gate, *up;            // dh: the saved pre-activations (M, N)
+  int save;                         // gate/up: store them
   int act;
   int* status;
 };
@@ -165,16 +181,47 @@ __device__ __forceinline__ uint4 pack8(const float* v) {
                     pack2<T>(v[6], v[7]));
 }
 
-template <bool PAIR>
-__host__ __device__ constexpr size_t dense_smem_bytes() {
-  return 1024 + size_t(kDgStages) * kDgStageBytes + 256;
+// TMA store of one staged chunk, and its bookkeeping (by one thread).
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t src, int32_t x,
+                                             int32_t y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(src), "r"(x), "r"(y)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() {
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void bulk_wait_all() {
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+// Barrier of the four epilogue warps.
+__device__ __forceinline__ void epilogue_barrier() {
+  asm volatile("bar.sync 1, 128;" ::: "memory");
+}
+
+// Byte offset of the 16-byte piece c of row r in a staged chunk (the 128- or 64-byte TMA
+// swizzle for rows of 128 or 64 bytes).
+template <int CHUNK>
+__device__ __forceinline__ uint32_t staged(int r, int c) {
+  return CHUNK == 64 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+}
+__device__ __forceinline__ void st_shared_16(uint32_t addr, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z),
+               "r"(v.w)
+               : "memory");
 }
 
 template <typename T, int EPI, bool PAIR>
 __global__ void __launch_bounds__(kDgThreads, 1)
     dense_gemm_kernel(const __grid_constant__ DenseMaps maps,
                       const __grid_constant__ DenseParams P) {
-  constexpr int kS = kDgStages;
+  using Cfg = DenseCfg<EPI>;
+  constexpr int kS = Cfg::kStages;
   constexpr int kTileM = PAIR ? 256 : 128;
   constexpr int kAcc = PAIR ? 256 : 128;            // accumulator columns of a tile
   constexpr int kTmem = 2 * kAcc;
@@ -182,7 +229,8 @@ __global__ void __launch_bounds__(kDgThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + size_t(kS) * kDgStageBytes);
+  uint8_t* staging = smem + size_t(kS) * kDgStageBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(staging + 2 * Cfg::kSetBytes);
   uint64_t* full_bar = bars;
   uint64_t* empty_bar = bars + kS;
   uint64_t* tfull_bar = bars + 2 * kS;
@@ -369,104 +417,146 @@ __global__ void __launch_bounds__(kDgThreads, 1)
     const int quarter = warp & 3;
     const int r = quarter * 32 + lane;
     const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
-    int acc = 0;
+    const uint32_t stage0 = smem_u32(staging);
+    constexpr int kCh = Cfg::kChunk;
+    const bool storer = threadIdx.x == 64;            // first thread of warp 2
+    int acc = 0, set = 0;
     uint32_t acc_ph = 0;
     for (int it = 0;; ++it) {
       const int tile = tile_of(P, worker, workers, it);
       if (tile >= P.total_tiles) break;
       const DenseTile tc = decode_dense(P, tile);
       const DenseProblem& q = P.p[tc.p];
-      bool ok = mbar_wait(smem_u32(&tfull_bar[acc]), acc_ph, s_abort);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) {
-        if (lane == 0) raise_abort(s_abort, P.status);
-        break;
-      }
-      tc_fence_after_sync();
-      const long long row = static_cast<long long>(tc.m) * kTileM + half * 128 + r;
+      const int rows0 = tc.m * kTileM + half * 128;   // first row of this CTA's part
+      const long long row = static_cast<long long>(rows0) + r;
       const bool row_ok = row < q.M;
       const int col0 = tc.n * kOutCols;
       const uint32_t tbase = lane_base + static_cast<uint32_t>(acc * kAcc);
+      const int cols = min(kOutCols, q.N - col0);
+      // dh: the saved pre-activations of a chunk are loaded one chunk ahead
+      uint4 g4[4], u4[4];
+      auto load_saved = [&](int c) {
+        const long long at = row * q.N + col0 + c;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const bool in = row_ok && c + v * 8 < cols;
+          g4[v] = in ? *reinterpret_cast<const uint4*>(static_cast<const T*>(P.gate) + at + v * 8)
+                     : make_uint4(0, 0, 0, 0);
+          u4[v] = in ? *reinterpret_cast<const uint4*>(static_cast<const T*>(P.up) + at + v * 8)
+                     : make_uint4(0, 0, 0, 0);
+        }
+      };
+      if (EPI == kGemmGluBackward) load_saved(0);
+      bool ok = mbar_wait(smem_u32(&tfull_bar[acc]), acc_ph, s_abort);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok && lane == 0) raise_abort(s_abort, P.status);
+      // The four warps leave together (they meet at named barriers below): the vote is
+      // carried by the barrier itself.
+      int all_ok;
+      asm volatile(
+          "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+          "barrier.cta.red.and.pred q, 1, 128, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+          : "=r"(all_ok)
+          : "r"(ok ? 1 : 0)
+          : "memory");
+      if (!all_ok) break;
+      tc_fence_after_sync();
 #pragma unroll 1
-      for (int c = 0; c < kOutCols; c += 32) {
-        if (col0 + c >= q.N) break;
+      for (int c = 0; c < cols; c += kCh) {
+        const uint32_t buf = stage0 + set * Cfg::kSetBytes;
         uint32_t a[32];
+        uint4 packed[Cfg::kOuts][kCh / 8];
         if (EPI == kGemmGluForward) {
           uint32_t u[32];
           tmem_ld_32cols(tbase + c, a);
           tmem_ld_32cols(tbase + kOutCols + c, u);
           tmem_ld_wait();
-          const long long at = row * q.N + col0 + c;
 #pragma unroll
           for (int v = 0; v < 4; ++v) {
-            if (row_ok && col0 + c + v * 8 < q.N) {
-              float h[8];
-              const float* ga = reinterpret_cast<const float*>(a) + v * 8;
-              const float* ua = reinterpret_cast<const float*>(u) + v * 8;
+            float h[8];
+            const float* ga = reinterpret_cast<const float*>(a) + v * 8;
+            const float* ua = reinterpret_cast<const float*>(u) + v * 8;
 #pragma unroll
-              for (int j = 0; j < 8; ++j) h[j] = act_value(ga[j], P.act) * ua[j];
-              *reinterpret_cast<uint4*>(static_cast<T*>(P.hidden) + at + v * 8) = pack8<T>(h);
-              if (P.gate) {
-                *reinterpret_cast<uint4*>(static_cast<T*>(P.gate) + at + v * 8) = pack8<T>(ga);
-                *reinterpret_cast<uint4*>(static_cast<T*>(P.up) + at + v * 8) = pack8<T>(ua);
-              }
-            }
+            for (int j = 0; j < 8; ++j) h[j] = act_value(ga[j], P.act) * ua[j];
+            packed[0][v] = pack8<T>(h);
+            packed[1 % Cfg::kOuts][v] = pack8<T>(ga);
+            packed[2 % Cfg::kOuts][v] = pack8<T>(ua);
           }
         } else if (EPI == kGemmGluBackward) {
-          const long long at = row * q.N + col0 + c;
-          uint4 g4[4], u4[4];
-#pragma unroll
-          for (int v = 0; v < 4; ++v)
-            if (row_ok && col0 + c + v * 8 < q.N) {
-              g4[v] = *reinterpret_cast<const uint4*>(static_cast<const T*>(P.gate) + at + v * 8);
-              u4[v] = *reinterpret_cast<const uint4*>(static_cast<const T*>(P.up) + at + v * 8);
-            }
           tmem_ld_32cols(tbase + c, a);
           tmem_ld_wait();
 #pragma unroll
           for (int v = 0; v < 4; ++v) {
-            if (row_ok && col0 + c + v * 8 < q.N) {
-              const uint32_t gw[4] = {g4[v].x, g4[v].y, g4[v].z, g4[v].w};
-              const uint32_t uw[4] = {u4[v].x, u4[v].y, u4[v].z, u4[v].w};
-              float dg[8], du[8], h[8];
+            const uint32_t gw[4] = {g4[v].x, g4[v].y, g4[v].z, g4[v].w};
+            const uint32_t uw[4] = {u4[v].x, u4[v].y, u4[v].z, u4[v].w};
+            float dg[8], du[8], h[8];
 #pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                const float2 gp = unpack2<T>(gw[j >> 1]), upv = unpack2<T>(uw[j >> 1]);
-                const float g = j & 1 ? gp.y : gp.x, u = j & 1 ? upv.y : upv.x;
-                const float dh = __uint_as_float(a[v * 8 + j]);
-                float val, der;
-                act_value_grad(g, P.act, val, der);
-                dg[j] = dh * u * der;
-                du[j] = dh * val;
-                h[j] = val * u;
-              }
-              *reinterpret_cast<uint4*>(static_cast<T*>(P.dgate) + at + v * 8) = pack8<T>(dg);
-              *reinterpret_cast<uint4*>(static_cast<T*>(P.dup) + at + v * 8) = pack8<T>(du);
-              *reinterpret_cast<uint4*>(static_cast<T*>(P.hidden) + at + v * 8) = pack8<T>(h);
+            for (int j = 0; j < 8; ++j) {
+              const float2 gp = unpack2<T>(gw[j >> 1]), upv = unpack2<T>(uw[j >> 1]);
+              const float g = j & 1 ? gp.y : gp.x, u = j & 1 ? upv.y : upv.x;
+              const float dh = __uint_as_float(a[v * 8 + j]);
+              float val, der;
+              act_value_grad(g, P.act, val, der);
+              dg[j] = dh * u * der;
+              du[j] = dh * val;
+              h[j] = val * u;
+            }
+            packed[0][v] = pack8<T>(h);
+            packed[1 % Cfg::kOuts][v] = pack8<T>(dg);
+            packed[2 % Cfg::kOuts][v] = pack8<T>(du);
+          }
+          if (c + kCh < cols) load_saved(c + kCh);
+        } else {
+#pragma unroll
+          for (int hh = 0; hh < kCh / 32; ++hh) {
+            tmem_ld_32cols(tbase + c + hh * 32, a);
+            tmem_ld_wait();
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+              packed[0][(hh * 4 + v) % (kCh / 8)] =
+                  pack8<T>(reinterpret_cast<const float*>(a) + v * 8);
+          }
+        }
+        if (c + kCh >= cols) {        // the accumulator is read: the next tile may have it
+          tc_fence_before_sync();
+          if (PAIR && !leader)
+            mbar_arrive_cluster(mapa_shared(smem_u32(&tempty_bar[acc]), 0));
+          else
+            mbar_arrive(smem_u32(&tempty_bar[acc]));
+        }
+        // this set's previous stores (two chunks ago) have read it
+        if (storer) bulk_wait_read<1>();
+        __syncwarp();
+        epilogue_barrier();
+#pragma unroll
+        for (int o = 0; o < Cfg::kOuts; ++o) {
+          if (EPI == kGemmGluForward && o > 0 && !P.save) break;
+#pragma unroll
+          for (int v = 0; v < kCh / 8; ++v)
+            st_shared_16(buf + o * Cfg::kBufBytes + staged<kCh>(r, v), packed[o][v]);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        epilogue_barrier();
+        if (storer) {
+          if (rows0 < q.M) {
+#pragma unroll
+            for (int o = 0; o < Cfg::kOuts; ++o) {
+              if (EPI == kGemmGluForward && o > 0 && !P.save) break;
+              tma_store_2d(&maps.m[q.map_out[o]], buf + o * Cfg::kBufBytes, col0 + c, rows0);
             }
           }
-        } else {
-          tmem_ld_32cols(tbase + c, a);
-          tmem_ld_wait();
-          T* out = static_cast<T*>(q.out) + row * q.ldo + col0 + c;
-#pragma unroll
-          for (int v = 0; v < 4; ++v)
-            if (row_ok && col0 + c + v * 8 < q.N)
-              *reinterpret_cast<uint4*>(out + v * 8) =
-                  pack8<T>(reinterpret_cast<const float*>(a) + v * 8);
+          bulk_commit();
         }
-        __syncwarp();               // the next TMEM load is a warp-wide instruction
+        __syncwarp();
+        set ^= 1;
       }
-      tc_fence_before_sync();
-      if (PAIR && !leader)
-        mbar_arrive_cluster(mapa_shared(smem_u32(&tempty_bar[acc]), 0));
-      else
-        mbar_arrive(smem_u32(&tempty_bar[acc]));
       if (++acc == 2) {
         acc = 0;
         acc_ph ^= 1u;
       }
     }
+    if (storer) bulk_wait_all();
+    __syncwarp();
   }
 
   tc_fence_before_sync();

@@ -12,6 +12,7 @@
 #include "dense_gemm_sm100.cuh"
 #include "moe_ffn.h"
 #include "ops_host.h"
+#include "stream_gemm_sm100.cuh"
 
 namespace {
 
@@ -37,15 +38,32 @@ int cuda_error(cudaError_t e, const char* what) {
   return set_error(MOE_CUDA_ERROR, buf);
 }
 
+template <typename T, int EPI, int NB>
+cudaError_t set_stream_smem_one() {
+  return cudaFuncSetAttribute(moe::stream_gemm_kernel<T, EPI, NB>,
+                              cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              int(moe::StreamCfg<NB>::kSmem));
+}
+
+template <typename T, int EPI>
+cudaError_t set_stream_smem() {
+  cudaError_t e = set_stream_smem_one<T, EPI, 16>();
+  if (e == cudaSuccess) e = set_stream_smem_one<T, EPI, 32>();
+  if (e == cudaSuccess) e = set_stream_smem_one<T, EPI, 64>();
+  if (e == cudaSuccess) e = set_stream_smem_one<T, EPI, 128>();
+  return e;
+}
+
 template <typename T, int EPI>
 cudaError_t set_smem() {
   cudaError_t e = cudaFuncSetAttribute(moe::dense_gemm_kernel<T, EPI, true>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       int(moe::dense_smem_bytes<true>()));
+                                       int(moe::DenseCfg<EPI>::kSmem));
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(moe::dense_gemm_kernel<T, EPI, false>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             int(moe::dense_smem_bytes<false>()));
+                             int(moe::DenseCfg<EPI>::kSmem));
+  if (e == cudaSuccess) e = set_stream_smem<T, EPI>();
   return e;
 }
 
@@ -88,6 +106,23 @@ bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) &
 size_t align_up(size_t v) { return (v + 255) / 256 * 256; }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// Matrix (rows, cols) of a 16-bit type, rows `ld` elements apart, in boxes of 64 (or 32)
+// columns x box_rows rows, swizzled over a box row's 128 (or 64) bytes; what a box covers
+// beyond the matrix reads as zero and is not written.
+bool encode_map(CUtensorMap* m, int half, const void* base, int64_t rows, int64_t cols, int64_t ld,
+                int box_rows, int box_cols = 64) {
+  cuuint64_t dims[2] = {cuuint64_t(cols), cuuint64_t(rows)};
+  cuuint64_t strides[1] = {cuuint64_t(ld) * 2};
+  cuuint32_t box[2] = {cuuint32_t(box_cols), cuuint32_t(box_rows)};
+  cuuint32_t estr[2] = {1, 1};
+  return moe::tensor_map_encoder()(
+             m, half ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+             const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // One launch being put together: tensor maps and products.
 struct GemmLaunch {
   moe::DenseMaps maps;
@@ -96,25 +131,14 @@ struct GemmLaunch {
   int half;                 // 16-bit type: 1 fp16, 0 bf16
   bool ok = true;
 
-  // Matrix (rows, cols), rows `ld` elements apart, in boxes of 64 columns x box_rows rows;
-  // what a box covers beyond the matrix reads as zero.
-  int map(const void* base, int64_t rows, int64_t cols, int64_t ld, int box_rows) {
-    cuuint64_t dims[2] = {cuuint64_t(cols), cuuint64_t(rows)};
-    cuuint64_t strides[1] = {cuuint64_t(ld) * 2};
-    cuuint32_t box[2] = {64, cuuint32_t(box_rows)};
-    cuuint32_t estr[2] = {1, 1};
-    ok = ok && moe::tensor_map_encoder()(
-                   &maps.m[n_maps],
-                   half ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
-                   const_cast<void*>(base), dims, strides, box, estr,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  int map(const void* base, int64_t rows, int64_t cols, int64_t ld, int box_rows,
+          int box_cols = 64) {
+    ok = ok && encode_map(&maps.m[n_maps], half, base, rows, cols, ld, box_rows, box_cols);
     return n_maps++;
   }
 
   void product(int M, int N, int tile_m, int tile_n, int64_t k0, int64_t k1, int a0, int a1,
-               int b0, int b1, int a_mn, int b_mn, void* out, int64_t ldo) {
+               int b0, int b1, int a_mn, int b_mn, int out0, int out1 = 0, int out2 = 0) {
     moe::DenseProblem& q = P.p[P.n_problems++];
     q.M = M;
     q.N = N;
@@ -129,8 +153,9 @@ struct GemmLaunch {
     q.map_b[1] = b1;
     q.a_mn = a_mn;
     q.b_mn = b_mn;
-    q.out = out;
-    q.ldo = ldo;
+    q.map_out[0] = out0;
+    q.map_out[1] = out1;
+    q.map_out[2] = out2;
     P.total_tiles += q.m_tiles * q.n_tiles;
   }
 };
@@ -153,7 +178,7 @@ cudaError_t launch(GemmLaunch& L, const DeviceInfo& d, cudaStream_t st) {
   L.P.status = d.status;
   return launch_overlapped(moe::dense_gemm_kernel<T, EPI, PAIR>,
                            dim3(PAIR ? 2 * workers : workers), dim3(moe::kDgThreads),
-                           moe::dense_smem_bytes<PAIR>(), st, PAIR ? 2 : 1, L.maps, L.P);
+                           moe::DenseCfg<EPI>::kSmem, st, PAIR ? 2 : 1, L.maps, L.P);
 }
 
 template <int EPI>
@@ -167,6 +192,51 @@ cudaError_t launch_any(GemmLaunch& L, bool pair, const DeviceInfo& d, cudaStream
 // CTA pairs on 256 x 256 tiles once there are enough of them for every pair of SMs.
 bool use_pairs(int64_t m, int64_t n, int cols, const DeviceInfo& d) {
   return ceil_div(m, 256) * ceil_div(n, cols) >= d.sms / 2;
+}
+
+// One product over at most 128 tokens: weights streamed by clusters that split the
+// reduction until there are about two CTAs an SM.
+struct StreamLaunch {
+  moe::StreamMaps maps;
+  moe::StreamParams P = {};
+  int half;
+  bool ok = true;
+
+  int columns() const { return P.T <= 16 ? 16 : P.T <= 32 ? 32 : P.T <= 64 ? 64 : 128; }
+  void weights(int i, const void* base, int64_t rows, int64_t cols, int box_rows) {
+    ok = ok && encode_map(&maps.a[i], half, base, rows, cols, cols, box_rows);
+  }
+  void tokens(int i, const void* base, int64_t cols, int64_t ld) {
+    ok = ok && encode_map(&maps.b[i], half, base, P.T, cols, ld, columns());
+  }
+};
+
+template <typename T, int EPI, int NB>
+cudaError_t launch_stream_columns(StreamLaunch& L, const DeviceInfo& d, cudaStream_t st) {
+  const int tiles = int(ceil_div(L.P.N, EPI == moe::kGemmGluForward ? 64 : 128));
+  const int total = L.P.kb[0] + L.P.kb[1];
+  int ranks = 1;
+  while (ranks < 8 && tiles * ranks * 2 <= 2 * d.sms && ranks * 2 <= total) ranks *= 2;
+  L.P.status = d.status;
+  return launch_overlapped(moe::stream_gemm_kernel<T, EPI, NB>, dim3(unsigned(tiles * ranks)),
+                           dim3(moe::kStreamThreads), moe::StreamCfg<NB>::kSmem, st, ranks, L.maps,
+                           L.P);
+}
+
+template <int EPI>
+cudaError_t launch_stream(StreamLaunch& L, const DeviceInfo& d, cudaStream_t st) {
+  if (!L.ok) return cudaErrorInvalidValue;
+  const int nb = L.columns();
+  if (L.half) {
+    if (nb == 16) return launch_stream_columns<__half, EPI, 16>(L, d, st);
+    if (nb == 32) return launch_stream_columns<__half, EPI, 32>(L, d, st);
+    if (nb == 64) return launch_stream_columns<__half, EPI, 64>(L, d, st);
+    return launch_stream_columns<__half, EPI, 128>(L, d, st);
+  }
+  if (nb == 16) return launch_stream_columns<__nv_bfloat16, EPI, 16>(L, d, st);
+  if (nb == 32) return launch_stream_columns<__nv_bfloat16, EPI, 32>(L, d, st);
+  if (nb == 64) return launch_stream_columns<__nv_bfloat16, EPI, 64>(L, d, st);
+  return launch_stream_columns<__nv_bfloat16, EPI, 128>(L, d, st);
 }
 
 int check_shape(int act, int dtype, int64_t T, int64_t d, int64_t f) {
@@ -227,6 +297,35 @@ int moe_gated_ffn_forward(int act, int dtype, int64_t T, int64_t d, int64_t f, c
   if (int s = device_info(&dev)) return s;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int m = int(T);
+  if (T <= moe::kStreamMaxTokens) {
+    StreamLaunch up_gemm;
+    up_gemm.half = dtype == MOE_DTYPE_FP16;
+    up_gemm.P.T = m;
+    up_gemm.P.N = int(f);
+    up_gemm.P.kb[0] = int(ceil_div(d, 64));
+    up_gemm.P.act = act;
+    up_gemm.P.hidden = workspace;
+    up_gemm.P.gate = gate;
+    up_gemm.P.up = up;
+    up_gemm.weights(0, W1, f, d, 64);
+    up_gemm.weights(1, W3, f, d, 64);
+    up_gemm.tokens(0, x, d, ldx);
+    cudaError_t e = launch_stream<moe::kGemmGluForward>(up_gemm, *dev, st);
+    if (e != cudaSuccess) return cuda_error(e, "gated feed-forward gate/up launch");
+    StreamLaunch down;
+    down.half = up_gemm.half;
+    down.P.T = m;
+    down.P.N = int(d);
+    down.P.kb[0] = int(ceil_div(f, 64));
+    down.P.early = 1;
+    down.P.out = out;
+    down.P.ldo = ldo;
+    down.weights(0, W2, d, f, 128);
+    down.tokens(0, workspace, f, f);
+    e = launch_stream<moe::kGemmPlain>(down, *dev, st);
+    if (e != cudaSuccess) return cuda_error(e, "gated feed-forward down launch");
+    return MOE_OK;
+  }
   {
     GemmLaunch L;
     L.half = dtype == MOE_DTYPE_FP16;
@@ -234,11 +333,12 @@ int moe_gated_ffn_forward(int act, int dtype, int64_t T, int64_t d, int64_t f, c
     const int a = L.map(x, T, d, ldx, 128);
     const int b1 = L.map(W1, f, d, d, pair ? 128 : 64);
     const int b3 = L.map(W3, f, d, d, pair ? 128 : 64);
+    const int o0 = L.map(workspace, T, f, f, 128, 32);
+    const int o1 = gate ? L.map(gate, T, f, f, 128, 32) : o0;
+    const int o2 = gate ? L.map(up, T, f, f, 128, 32) : o0;
     if (!L.ok) return set_error(MOE_CUDA_ERROR, "tensor map encoding failed");
-    L.product(m, int(f), pair ? 256 : 128, pair ? 128 : 64, d, 0, a, a, b1, b3, 0, 0, nullptr, 0);
-    L.P.hidden = workspace;
-    L.P.gate = gate;
-    L.P.up = up;
+    L.product(m, int(f), pair ? 256 : 128, pair ? 128 : 64, d, 0, a, a, b1, b3, 0, 0, o0, o1, o2);
+    L.P.save = gate != nullptr;
     L.P.act = act;
     const cudaError_t e = launch_any<moe::kGemmGluForward>(L, pair, *dev, st);
     if (e != cudaSuccess) return cuda_error(e, "gated feed-forward gate/up launch");
@@ -248,9 +348,10 @@ int moe_gated_ffn_forward(int act, int dtype, int64_t T, int64_t d, int64_t f, c
   const bool pair = use_pairs(T, d, 256, *dev);
   const int a = L.map(workspace, T, f, f, 128);
   const int b = L.map(W2, d, f, f, 128);
+  const int o = L.map(out, T, d, ldo, 128);
   if (!L.ok) return set_error(MOE_CUDA_ERROR, "tensor map encoding failed");
   const int tile = pair ? 256 : 128;
-  L.product(m, int(d), tile, tile, f, 0, a, a, b, b, 0, 0, out, ldo);
+  L.product(m, int(d), tile, tile, f, 0, a, a, b, b, 0, 0, o);
   const cudaError_t e = launch_any<moe::kGemmPlain>(L, pair, *dev, st);
   if (e != cudaSuccess) return cuda_error(e, "gated feed-forward down launch");
   return MOE_OK;
@@ -295,20 +396,55 @@ int moe_gated_ffn_backward(int act, int dtype, int64_t T, int64_t d, int64_t f, 
   char* ws = static_cast<char*>(workspace);
   void *dgate = ws, *dup = ws + plane, *hidden = ws + 2 * plane;
   const int m = int(T);
-  {
+  const bool stream_path = T <= moe::kStreamMaxTokens;
+  if (stream_path) {
+    StreamLaunch dh;
+    dh.half = dtype == MOE_DTYPE_FP16;
+    dh.P.T = m;
+    dh.P.N = int(f);
+    dh.P.kb[0] = int(ceil_div(d, 64));
+    dh.P.a_mn = 1;
+    dh.P.act = act;
+    dh.P.gate = const_cast<void*>(gate);
+    dh.P.up = const_cast<void*>(up);
+    dh.P.dgate = dgate;
+    dh.P.dup = dup;
+    dh.P.hidden = hidden;
+    dh.weights(0, W2, d, f, 64);
+    dh.tokens(0, dout, d, lddout);
+    cudaError_t e = launch_stream<moe::kGemmGluBackward>(dh, *dev, st);
+    if (e != cudaSuccess) return cuda_error(e, "gated feed-forward dh launch");
+    if (dx) {
+      StreamLaunch gx;
+      gx.half = dh.half;
+      gx.P.T = m;
+      gx.P.N = int(d);
+      gx.P.kb[0] = gx.P.kb[1] = int(ceil_div(f, 64));
+      gx.P.a_mn = 1;
+      gx.P.early = 1;
+      gx.P.out = dx;
+      gx.P.ldo = lddx;
+      gx.weights(0, W1, f, d, 64);
+      gx.weights(1, W3, f, d, 64);
+      gx.tokens(0, dgate, f, f);
+      gx.tokens(1, dup, f, f);
+      e = launch_stream<moe::kGemmPlain>(gx, *dev, st);
+      if (e != cudaSuccess) return cuda_error(e, "gated feed-forward dx launch");
+    }
+    if (!dW1 && !dW3 && !dW2) return MOE_OK;
+  } else {
     GemmLaunch L;
     L.half = dtype == MOE_DTYPE_FP16;
     const bool pair = use_pairs(T, f, 256, *dev);
     const int a = L.map(dout, T, d, lddout, 128);
     const int b = L.map(W2, d, f, f, 64);
+    const int o0 = L.map(hidden, T, f, f, 128, 32), o1 = L.map(dgate, T, f, f, 128, 32);
+    const int o2 = L.map(dup, T, f, f, 128, 32);
     if (!L.ok) return set_error(MOE_CUDA_ERROR, "tensor map encoding failed");
     const int tile = pair ? 256 : 128;
-    L.product(m, int(f), tile, tile, d, 0, a, a, b, b, 0, 1, nullptr, 0);
-    L.P.gate = const_cast<void*>(gate);
-    L.P.up = const_cast<void*>(up);
-    L.P.dgate = dgate;
-    L.P.dup = dup;
-    L.P.hidden = hidden;
+    L.product(m, int(f), tile, tile, d, 0, a, a, b, b, 0, 1, o0, o1, o2);
+    L.P.gate = gate;
+    L.P.up = up;
     L.P.act = act;
     const cudaError_t e = launch_any<moe::kGemmGluBackward>(L, pair, *dev, st);
     if (e != cudaSuccess) return cuda_error(e, "gated feed-forward dh launch");
@@ -317,23 +453,25 @@ int moe_gated_ffn_backward(int act, int dtype, int64_t T, int64_t d, int64_t f, 
   L.half = dtype == MOE_DTYPE_FP16;
   const bool pair = use_pairs(f, d, 256, *dev);
   const int tile = pair ? 256 : 128;
-  if (dx) {
+  if (dx && !stream_path) {
     const int a0 = L.map(dgate, T, f, f, 128), a1 = L.map(dup, T, f, f, 128);
     const int b0 = L.map(W1, f, d, d, 64), b1 = L.map(W3, f, d, d, 64);
-    L.product(m, int(d), tile, tile, f, f, a0, a1, b0, b1, 0, 1, dx, lddx);
+    L.product(m, int(d), tile, tile, f, f, a0, a1, b0, b1, 0, 1, L.map(dx, T, d, lddx, 128));
   }
   const int xm = dW1 || dW3 ? L.map(x, T, d, ldx, 64) : 0;
   if (dW1) {
     const int a = L.map(dgate, T, f, f, 64);
-    L.product(int(f), int(d), tile, tile, T, 0, a, a, xm, xm, 1, 1, dW1, d);
+    L.product(int(f), int(d), tile, tile, T, 0, a, a, xm, xm, 1, 1,
+              L.map(dW1, f, d, d, 128));
   }
   if (dW3) {
     const int a = L.map(dup, T, f, f, 64);
-    L.product(int(f), int(d), tile, tile, T, 0, a, a, xm, xm, 1, 1, dW3, d);
+    L.product(int(f), int(d), tile, tile, T, 0, a, a, xm, xm, 1, 1,
+              L.map(dW3, f, d, d, 128));
   }
   if (dW2) {
     const int a = L.map(dout, T, d, lddout, 64), b = L.map(hidden, T, f, f, 64);
-    L.product(int(d), int(f), tile, tile, T, 0, a, a, b, b, 1, 1, dW2, f);
+    L.product(int(d), int(f), tile, tile, T, 0, a, a, b, b, 1, 1, L.map(dW2, d, f, f, 128));
   }
   if (!L.ok) return set_error(MOE_CUDA_ERROR, "tensor map encoding failed");
   const cudaError_t e = launch_any<moe::kGemmPlain>(L, pair, *dev, st);
