@@ -18,10 +18,24 @@
 
 namespace moe {
 
-__device__ __forceinline__ uint4 philox_4x32_10(uint64_t block, uint64_t offset, uint64_t seed) {
-  uint32_t c0 = static_cast<uint32_t>(block), c1 = static_cast<uint32_t>(block >> 32);
-  uint32_t c2 = static_cast<uint32_t>(offset), c3 = static_cast<uint32_t>(offset >> 32);
-  uint32_t k0 = static_cast<uint32_t>(seed), k1 = static_cast<uint32_t>(seed >> 32);
+// Seed and offset, the same in every thread: told to the compiler by the shuffle, so that
+// the key schedule is uniform arithmetic and not part of each thread's.
+struct PhiloxKey {
+  uint32_t k0, k1, o0, o1;
+};
+__device__ __forceinline__ PhiloxKey load_philox_key(const unsigned long long* rng) {
+  const unsigned long long seed = rng[0], offset = rng[1];
+  PhiloxKey k;
+  k.k0 = __shfl_sync(0xffffffffu, static_cast<uint32_t>(seed), 0);
+  k.k1 = __shfl_sync(0xffffffffu, static_cast<uint32_t>(seed >> 32), 0);
+  k.o0 = __shfl_sync(0xffffffffu, static_cast<uint32_t>(offset), 0);
+  k.o1 = __shfl_sync(0xffffffffu, static_cast<uint32_t>(offset >> 32), 0);
+  return k;
+}
+
+__device__ __forceinline__ uint4 philox_4x32_10(uint32_t c0, uint32_t c1, const PhiloxKey& key) {
+  uint32_t c2 = key.o0, c3 = key.o1;
+  uint32_t k0 = key.k0, k1 = key.k1;
 #pragma unroll
   for (int r = 0; r < 10; ++r) {
     const uint64_t p0 = static_cast<uint64_t>(c0) * 0xD2511F53u;
@@ -40,87 +54,138 @@ struct DropoutParams {
   const void* x;          // x (forward) or dout (backward)
   const void* residual;   // null: none
   void* out;
-  long long n, cols;      // rows * cols elements
+  long long n, cols;      // rows * cols elements (of this launch)
+  uint32_t block_lo, block_hi;     // flat: Philox block of the launch's first element
   long long ldx, ldr, ldo;
   const unsigned long long* rng;   // device: seed, offset
-  uint32_t threshold;     // a word below it drops its element (p < 1)
+  uint32_t threshold;     // a word below it drops its element (kDropDraw)
   float scale;            // 1 / (1 - p)
-  int mode;               // 0: p = 0, nothing dropped; 1: draw; 2: p = 1, all dropped
 };
 
+// p = 0 keeps all, p = 1 drops all; only what lies between draws.
+enum { kDropNone = 0, kDropDraw = 1, kDropAll = 2 };
+
+template <int MODE>
+__device__ __forceinline__ bool drop_keeps(uint32_t word, uint32_t threshold) {
+  return MODE == kDropNone || (MODE == kDropDraw && word >= threshold);
+}
+
+// One element, any type and mode.
+template <typename T, bool RES, int MODE>
+__device__ __forceinline__ T drop_element(const DropoutParams& P, T x, T res, uint32_t word) {
+  const float v = drop_keeps<MODE>(word, P.threshold) ? to_f32(x) : 0.0f;
+  return from_f32<T>(RES ? fmaf(v, P.scale, to_f32(res)) : v * P.scale);
+}
+
+// One 16-byte vector: its mask, product and sum.
+template <typename T, bool RES, int MODE>
+__device__ __forceinline__ uint4 drop_vector(const DropoutParams& P, uint32_t i,
+                                             const PhiloxKey& key, const uint4& a,
+                                             const uint4& r) {
+  const uint32_t av[4] = {a.x, a.y, a.z, a.w}, rv[4] = {r.x, r.y, r.z, r.w};
+  uint32_t ov[4];
+  if constexpr (sizeof(T) == 4) {
+    uint4 w = make_uint4(0, 0, 0, 0);
+    if (MODE == kDropDraw) w = philox_4x32_10(P.block_lo + i, P.block_hi, key);
+    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      ov[j] = __float_as_uint(drop_element<float, RES, MODE>(
+          P, __uint_as_float(av[j]), __uint_as_float(RES ? rv[j] : 0u), ws[j]));
+  } else {
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      uint4 w = make_uint4(0, 0, 0, 0);
+      if (MODE == kDropDraw) w = philox_4x32_10(P.block_lo + 2 * i + b, P.block_hi, key);
+      const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float2 x2 = unpack2<T>(av[2 * b + h]);
+        const float lo = drop_keeps<MODE>(ws[2 * h], P.threshold) ? x2.x : 0.0f;
+        const float hi = drop_keeps<MODE>(ws[2 * h + 1], P.threshold) ? x2.y : 0.0f;
+        float2 r2 = make_float2(0.0f, 0.0f);
+        if (RES) r2 = unpack2<T>(rv[2 * b + h]);
+        ov[2 * b + h] = RES ? pack2<T>(fmaf(lo, P.scale, r2.x), fmaf(hi, P.scale, r2.y))
+                            : pack2<T>(lo * P.scale, hi * P.scale);
+      }
+    }
+  }
+  return make_uint4(ov[0], ov[1], ov[2], ov[3]);
+}
+
 // Contiguous tensors (each row stride equal to cols): the batch is one line of n
-// elements, whatever cols is. A thread takes one 16-byte vector (2 Philox blocks of a
-// 16-bit type, 1 of fp32) per step.
-template <typename T, bool RES>
-__global__ void __launch_bounds__(256) dropout_flat_kernel(const DropoutParams P) {
+// elements, whatever cols is. A launch covers at most 2^33 of them, so that the Philox
+// block's high word is one number for the launch: with it and the offset uniform, the
+// first two rounds have one product a thread each instead of two. A block of 256 threads
+// takes VPT * 256 consecutive 16-byte vectors, a thread VPT of them 256 apart, all loaded
+// before the first is used. The kernel is bound by the integer and fp32 pipes about as
+// much as by memory (18 wide products and 20 exclusive ors for 4 elements): 8192 x 7168
+// bf16 forward and backward took 155 us at one vector a thread with the key schedule in
+// every thread, 113 us at four with it uniform.
+constexpr long long kDropSlice = 1LL << 33;
+template <typename T, bool RES, int MODE, int VPT>
+__global__ void __launch_bounds__(256, 4) dropout_flat_kernel(const DropoutParams P) {
   constexpr int V = 16 / sizeof(T);
-  pdl_launch_dependents();
   pdl_wait();
+  pdl_launch_dependents();
   const T* x = static_cast<const T*>(P.x);
   const T* res = static_cast<const T*>(P.residual);
   T* out = static_cast<T*>(P.out);
-  const uint64_t seed = P.mode == 1 ? P.rng[0] : 0, offset = P.mode == 1 ? P.rng[1] : 0;
-  const long long nvec = P.n / V;
-  const long long stride = static_cast<long long>(gridDim.x) * blockDim.x;
-  const long long first = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
-  for (long long i = first; i < nvec; i += stride) {
-    const Pack<T, V> a = load_pack<T, V>(x + i * V);
-    Pack<T, V> r;
-    if (RES) r = load_pack<T, V>(res + i * V);
-    Pack<T, V> o;
+  PhiloxKey key = {};
+  if (MODE == kDropDraw) key = load_philox_key(P.rng);
+  const uint32_t nvec = static_cast<uint32_t>(P.n / V);
+  const uint32_t base = blockIdx.x * (256 * VPT) + threadIdx.x;
+  uint4 a[VPT], r[VPT];
 #pragma unroll
-    for (int b = 0; b < V / 4; ++b) {
-      uint4 w = make_uint4(0, 0, 0, 0);
-      if (P.mode == 1) w = philox_4x32_10(i * (V / 4) + b, offset, seed);
-      const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const bool keep = P.mode == 0 || (P.mode == 1 && ws[j] >= P.threshold);
-        float v = keep ? to_f32(a.v[4 * b + j]) * P.scale : 0.0f;
-        if (RES) v += to_f32(r.v[4 * b + j]);
-        o.v[4 * b + j] = from_f32<T>(v);
-      }
+  for (int k = 0; k < VPT; ++k) {
+    const uint32_t i = base + k * 256;
+    if (i < nvec) {
+      a[k] = reinterpret_cast<const uint4*>(x)[i];
+      if (RES) r[k] = reinterpret_cast<const uint4*>(res)[i];
     }
-    store_pack<T, V>(out + i * V, o);
   }
-  // the last n % V elements, one a thread
-  const long long tail = nvec * V + first;
-  if (tail < P.n) {
+#pragma unroll
+  for (int k = 0; k < VPT; ++k) {
+    const uint32_t i = base + k * 256;
+    if (i < nvec)
+      reinterpret_cast<uint4*>(out)[i] = drop_vector<T, RES, MODE>(P, i, key, a[k], r[k]);
+  }
+  // the last n % V elements, by the first block
+  const long long tail = static_cast<long long>(nvec) * V + threadIdx.x;
+  if (blockIdx.x == 0 && tail < P.n) {
     uint4 w = make_uint4(0, 0, 0, 0);
-    if (P.mode == 1) w = philox_4x32_10(tail >> 2, offset, seed);
+    if (MODE == kDropDraw)
+      w = philox_4x32_10(P.block_lo + static_cast<uint32_t>(tail >> 2), P.block_hi, key);
     const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-    const bool keep = P.mode == 0 || (P.mode == 1 && ws[tail & 3] >= P.threshold);
-    float v = keep ? to_f32(x[tail]) * P.scale : 0.0f;
-    if (RES) v += to_f32(res[tail]);
-    out[tail] = from_f32<T>(v);
+    out[tail] = drop_element<T, RES, MODE>(P, x[tail], RES ? res[tail] : x[tail], ws[tail & 3]);
   }
 }
 
 // Any strides and alignment: a thread takes the four elements of one Philox block,
 // element by element.
-template <typename T, bool RES>
+template <typename T, bool RES, int MODE>
 __global__ void __launch_bounds__(256) dropout_strided_kernel(const DropoutParams P) {
-  pdl_launch_dependents();
   pdl_wait();
+  pdl_launch_dependents();
   const T* x = static_cast<const T*>(P.x);
   const T* res = static_cast<const T*>(P.residual);
   T* out = static_cast<T*>(P.out);
-  const uint64_t seed = P.mode == 1 ? P.rng[0] : 0, offset = P.mode == 1 ? P.rng[1] : 0;
+  PhiloxKey key = {};
+  if (MODE == kDropDraw) key = load_philox_key(P.rng);
   const long long nblk = (P.n + 3) / 4;
   const long long stride = static_cast<long long>(gridDim.x) * blockDim.x;
   for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < nblk;
        i += stride) {
     uint4 w = make_uint4(0, 0, 0, 0);
-    if (P.mode == 1) w = philox_4x32_10(i, offset, seed);
+    if (MODE == kDropDraw) w = philox_4x32_10(static_cast<uint32_t>(i), static_cast<uint32_t>(i >> 32), key);
     const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
     long long row = (4 * i) / P.cols, col = 4 * i - row * P.cols;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       if (4 * i + j >= P.n) break;
-      const bool keep = P.mode == 0 || (P.mode == 1 && ws[j] >= P.threshold);
-      float v = keep ? to_f32(x[row * P.ldx + col]) * P.scale : 0.0f;
-      if (RES) v += to_f32(res[row * P.ldr + col]);
-      out[row * P.ldo + col] = from_f32<T>(v);
+      const T a = x[row * P.ldx + col];
+      out[row * P.ldo + col] =
+          drop_element<T, RES, MODE>(P, a, RES ? res[row * P.ldr + col] : a, ws[j]);
       if (++col == P.cols) {
         col = 0;
         ++row;

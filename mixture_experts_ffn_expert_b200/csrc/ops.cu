@@ -158,17 +158,49 @@ int check_norm(int kind, int dtype, int wdtype, int64_t rows, int64_t cols) {
 }
 
 // ------------------------------------------------------------------ dropout
-template <typename T, bool RES>
-cudaError_t launch_dropout(const moe::DropoutParams& P, bool flat, cudaStream_t st) {
-  const int64_t per_thread = flat ? 16 / sizeof(T) : 4;
-  int64_t blocks = (P.n / per_thread + 255) / 256;
-  if (blocks < 1) blocks = 1;
-  if (blocks > (1 << 20)) blocks = 1 << 20;      // the rest of a larger tensor by stride
-  if (flat)
-    return launch_overlapped(moe::dropout_flat_kernel<T, RES>, dim3(unsigned(blocks)), dim3(256),
-                             0, st, 1, P);
-  return launch_overlapped(moe::dropout_strided_kernel<T, RES>, dim3(unsigned(blocks)), dim3(256),
-                           0, st, 1, P);
+template <typename T, bool RES, int MODE>
+cudaError_t launch_dropout(moe::DropoutParams P, bool flat, cudaStream_t st) {
+  if (!flat) {
+    int64_t blocks = (P.n + 1023) / 1024;
+    if (blocks > (1 << 20)) blocks = 1 << 20;      // the rest of a larger tensor by stride
+    return launch_overlapped(moe::dropout_strided_kernel<T, RES, MODE>, dim3(unsigned(blocks)),
+                             dim3(256), 0, st, 1, P);
+  }
+  const int64_t n = P.n;
+  const char *x = static_cast<const char*>(P.x), *res = static_cast<const char*>(P.residual);
+  char* out = static_cast<char*>(P.out);
+  for (int64_t e0 = 0; e0 < n; e0 += moe::kDropSlice) {
+    P.n = n - e0 < moe::kDropSlice ? n - e0 : moe::kDropSlice;
+    P.x = x + e0 * sizeof(T);
+    P.residual = RES ? res + e0 * sizeof(T) : nullptr;
+    P.out = out + e0 * sizeof(T);
+    P.block_lo = static_cast<uint32_t>(e0 >> 2);
+    P.block_hi = static_cast<uint32_t>((e0 >> 2) >> 32);
+    const int64_t vecs = P.n * sizeof(T) / 16;
+    // Four vectors a thread once that still leaves two rounds of blocks for every SM; below,
+    // one each (128 x 2048 bf16: 1.5 us against 2.3 with four).
+    cudaError_t e;
+    if (vecs >= 8 * 148 * 1024)
+      e = launch_overlapped(moe::dropout_flat_kernel<T, RES, MODE, 4>,
+                            dim3(unsigned((vecs + 1023) / 1024)), dim3(256), 0, st, 1, P);
+    else
+      e = launch_overlapped(moe::dropout_flat_kernel<T, RES, MODE, 1>,
+                            dim3(unsigned(vecs < 256 ? 1 : (vecs + 255) / 256)), dim3(256), 0, st,
+                            1, P);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+template <typename T>
+cudaError_t dropout_typed(const moe::DropoutParams& P, int mode, bool flat, cudaStream_t st) {
+  if (P.residual)
+    return mode == moe::kDropNone   ? launch_dropout<T, true, moe::kDropNone>(P, flat, st)
+           : mode == moe::kDropDraw ? launch_dropout<T, true, moe::kDropDraw>(P, flat, st)
+                                    : launch_dropout<T, true, moe::kDropAll>(P, flat, st);
+  return mode == moe::kDropNone   ? launch_dropout<T, false, moe::kDropNone>(P, flat, st)
+         : mode == moe::kDropDraw ? launch_dropout<T, false, moe::kDropDraw>(P, flat, st)
+                                  : launch_dropout<T, false, moe::kDropAll>(P, flat, st);
 }
 
 int dropout_run(int dtype, int64_t rows, int64_t cols, const void* x, int64_t ldx,
@@ -199,24 +231,18 @@ int dropout_run(int dtype, int64_t rows, int64_t cols, const void* x, int64_t ld
   P.ldo = ldo;
   P.rng = reinterpret_cast<const unsigned long long*>(rng);
   const double t = std::nearbyint(p * 4294967296.0);
-  P.mode = t >= 4294967296.0 ? 2 : t > 0.0 ? 1 : 0;
-  P.threshold = P.mode == 1 ? static_cast<uint32_t>(t) : 0u;
+  const int mode = t >= 4294967296.0 ? moe::kDropAll : t > 0.0 ? moe::kDropDraw : moe::kDropNone;
+  P.threshold = mode == moe::kDropDraw ? static_cast<uint32_t>(t) : 0u;
   P.scale = p < 1.0 ? static_cast<float>(1.0 / (1.0 - p)) : 0.0f;
-  if (P.mode == 1 && (!rng || !aligned(rng, 8)))
+  if (mode == moe::kDropDraw && (!rng || !aligned(rng, 8)))
     return set_error(MOE_INVALID_ARG, "rng must point to two uint64 on the device when p > 0");
   const bool flat = ldx == cols && ldo == cols && (!residual || ldr == cols) && aligned(x, 16) &&
                     aligned(out, 16) && (!residual || aligned(residual, 16));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e;
-  if (dtype == MOE_DTYPE_BF16)
-    e = residual ? launch_dropout<__nv_bfloat16, true>(P, flat, st)
-                 : launch_dropout<__nv_bfloat16, false>(P, flat, st);
-  else if (dtype == MOE_DTYPE_FP16)
-    e = residual ? launch_dropout<__half, true>(P, flat, st)
-                 : launch_dropout<__half, false>(P, flat, st);
-  else
-    e = residual ? launch_dropout<float, true>(P, flat, st)
-                 : launch_dropout<float, false>(P, flat, st);
+  const cudaError_t e = dtype == MOE_DTYPE_BF16
+                            ? dropout_typed<__nv_bfloat16>(P, mode, flat, st)
+                        : dtype == MOE_DTYPE_FP16 ? dropout_typed<__half>(P, mode, flat, st)
+                                                  : dropout_typed<float>(P, mode, flat, st);
   return launch_status(e, "dropout");
 }
 

@@ -6,10 +6,12 @@
 // tensor work does not grow with a padded token tile. The reduction is split over the CTAs
 // of a cluster (1, 2, 4 or 8), as many as it takes to give every SM a stream of its own:
 // two CTAs share an SM, each with its own ring of TMA stages, which keeps about 200 KB of
-// loads in flight an SM. Each CTA leaves its fp32 partial tile in its own shared memory;
-// after a cluster barrier every CTA adds an equal share of the rows over the ranks, in
-// rank order, through distributed shared memory, and runs the epilogue on them (so sums
-// are the same bits every time and no partial result goes through global memory).
+// loads in flight an SM. Every rank finishes an equal share of the tile's rows: each CTA
+// stores its fp32 partial rows from TMEM straight into the shared memory of the rank that
+// owns them (distributed shared memory), and after a cluster barrier that rank adds them
+// in rank order and runs the epilogue (so sums are the same bits every time and no partial
+// result goes through global memory). Stores, not loads, cross the cluster: with 128
+// tokens the ranks' loads of each other's partial tiles took 4 of the kernel's 11 us.
 //
 //   gate/up  A = W1 rows 0-63, W3 rows 64-127 of the tile    epilogue act(gate) * up
 //   down     A = W2                                          plain
@@ -27,11 +29,16 @@ constexpr int kStreamMaxTokens = 128;
 template <int NB>
 struct StreamCfg {
   static constexpr int kStageBytes = kDgTileBytes + NB * 128;
-  static constexpr int kStages = NB <= 16 ? 6 : NB <= 32 ? 5 : NB <= 64 ? 4 : 3;
-  static constexpr int kRedBytes = 128 * NB * 4;          // partial tile, over the stages
+  static constexpr int kStages = NB <= 16 ? 5 : NB <= 32 ? 4 : 3;
+  // Partial rows received from the ranks: an area of their own, or for 128 tokens (where
+  // that would leave no room for the stages of a second CTA) the stages, once every rank
+  // has finished its MMAs.
+  static constexpr bool kOverStages = NB == 128;
+  static constexpr int kRedBytes = 128 * NB * 4;
   static constexpr int kTmem = NB < 32 ? 32 : NB;
-  static constexpr size_t kSmem = 1024 + size_t(kStages) * kStageBytes + 256;
-  static_assert(kRedBytes <= kStages * kStageBytes, "the partial tile fits the stages");
+  static constexpr size_t kSmem =
+      1024 + size_t(kStages) * kStageBytes + (kOverStages ? 0 : kRedBytes) + 256;
+  static_assert(!kOverStages || kRedBytes <= kStages * kStageBytes, "they fit the stages");
 };
 
 struct StreamParams {
@@ -50,13 +57,8 @@ struct StreamMaps {
   CUtensorMap a[2], b[2];
 };
 
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
 __device__ __forceinline__ uint32_t cluster_nctarank() {
@@ -75,7 +77,10 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + size_t(kS) * Cfg::kStageBytes);
+  float* red = reinterpret_cast<float*>(
+      smem + (Cfg::kOverStages ? 0 : size_t(kS) * Cfg::kStageBytes));
+  uint64_t* full_bar = reinterpret_cast<uint64_t*>(
+      smem + size_t(kS) * Cfg::kStageBytes + (Cfg::kOverStages ? 0 : Cfg::kRedBytes));
   uint64_t* empty_bar = full_bar + kS;
   uint64_t* done_bar = empty_bar + kS;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(done_bar + 1);
@@ -105,7 +110,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
     tmem_relinquish();
   }
   tc_fence_before_sync();
-  __syncthreads();
+  cluster_sync();                  // the ranks' shared memory may be written from here on
   tc_fence_after_sync();
   const uint32_t tmem_base = *s_tmem;
 
@@ -197,27 +202,41 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
   // kernel is complete and a dependent may read the weights early.
   pdl_launch_dependents();
 
-  // ------------------------------------------------------------ partial tile to shared memory
-  // All MMAs are done, so all stages have been read; the tile is stored column (token) by
-  // column, 128 rows each: consecutive lanes write consecutive words.
-  if (warp >= 2 && warp < 6) {
+  // ------------------------------------------------------------ partial rows to their owners
+  const int share = kRows / ranks;                 // output columns a rank finishes
+  const int rows_each = 128 / ranks;               // accumulator rows of those
+  const bool finisher = warp >= 2 && warp < 6;
+  bool done = false;
+  if (finisher) {
     int never = 0;
-    bool ok = mbar_wait(smem_u32(done_bar), 0, &never);
-    ok = __all_sync(0xffffffffu, ok);
-    if (!ok && lane == 0) raise_abort(s_abort, P.status);
+    done = mbar_wait(smem_u32(done_bar), 0, &never);
+    done = __all_sync(0xffffffffu, done);
+    if (!done && lane == 0) raise_abort(s_abort, P.status);
     tc_fence_after_sync();
-    if (ok) {
+  }
+  if (Cfg::kOverStages) cluster_sync();            // all ranks' stages have been read
+  if (finisher) {
+    if (done) {
       const int quarter = warp & 3;
+      const int r = quarter * 32 + lane;           // accumulator row
       const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
-      float* red = reinterpret_cast<float*>(smem) + quarter * 32 + lane;
+      // gate/up: rows 64-127 are the up rows of the owners of rows 0-63
+      const int out_row = EPI == kGemmGluForward ? (r & 63) : r;
+      const int owner = out_row / share;
+      const int local = out_row - owner * share + (EPI == kGemmGluForward && r >= 64 ? share : 0);
+      // token by token, so that a warp's store is one run of consecutive words for every
+      // owner (16-byte stores of four tokens a lane, a row apart, took twice as long)
+      const uint32_t dst =
+          mapa_shared(smem_u32(red), owner) + (rank * P.T * rows_each + local) * 4;
 #pragma unroll 1
-      for (int c = 0; c < NB; c += 8) {
-        if (c >= P.T) break;
-        uint32_t v[8];
-        tmem_ld_8cols(lane_base + c, v);
+      for (int c = 0; c < P.T; c += 16) {
+        uint32_t v[16];
+        tmem_ld_8cols(lane_base + c, *reinterpret_cast<uint32_t(*)[8]>(v));
+        tmem_ld_8cols(lane_base + c + 8, *reinterpret_cast<uint32_t(*)[8]>(v + 8));
         tmem_ld_wait();
 #pragma unroll
-        for (int j = 0; j < 8; ++j) red[(c + j) * 128] = __uint_as_float(v[j]);
+        for (int j = 0; j < 16; ++j)
+          if (c + j < P.T) st_cluster_f32(dst + (c + j) * rows_each * 4, v[j]);
       }
     }
     tc_fence_before_sync();
@@ -225,38 +244,29 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
   cluster_sync();
 
   // ------------------------------------------------------------ reduction and epilogue
-  // This CTA's share: rows r_lo .. r_lo + share - 1 of the tile's outputs, four at a time.
-  const int share = kRows / ranks;
-  const int r_lo = rank * share;
+  // This rank's share of the tile's output columns, four at a time.
   const int quads = share / 4;
-  const uint32_t red0 = smem_u32(smem);
   for (int i = threadIdx.x; i < P.T * quads; i += kStreamThreads) {
     const int t = i / quads;
-    const int r = r_lo + (i - t * quads) * 4;
-    const int n = row0 + r;
+    const int local = (i - t * quads) * 4;
+    const int n = row0 + rank * share + local;
     if (n >= P.N) continue;
+    const float* part = red + t * rows_each + local;
     float v[4] = {0, 0, 0, 0}, u[4] = {0, 0, 0, 0};
-    float4 p[8], w[8];               // all ranks' loads in flight before the first addition
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       if (k < ranks) {
-        const uint32_t base = mapa_shared(red0, k) + (t * 128 + r) * 4;
-        p[k] = ld_cluster_f4(base);
-        if (EPI == kGemmGluForward) w[k] = ld_cluster_f4(base + 64 * 4);
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      if (k < ranks) {
-        v[0] += p[k].x;
-        v[1] += p[k].y;
-        v[2] += p[k].z;
-        v[3] += p[k].w;
+        const float4 p = *reinterpret_cast<const float4*>(part + k * P.T * rows_each);
+        v[0] += p.x;
+        v[1] += p.y;
+        v[2] += p.z;
+        v[3] += p.w;
         if (EPI == kGemmGluForward) {
-          u[0] += w[k].x;
-          u[1] += w[k].y;
-          u[2] += w[k].z;
-          u[3] += w[k].w;
+          const float4 w = *reinterpret_cast<const float4*>(part + k * P.T * rows_each + share);
+          u[0] += w.x;
+          u[1] += w.y;
+          u[2] += w.z;
+          u[3] += w.w;
         }
       }
     }
@@ -300,7 +310,6 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
           make_uint2(pack2<T>(h[0], h[1]), pack2<T>(h[2], h[3]));
     }
   }
-  cluster_sync();                  // the other ranks have read this CTA's partial tile
   if (warp == 1) tmem_dealloc(tmem_base, Cfg::kTmem);
 }
 

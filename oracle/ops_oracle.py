@@ -88,10 +88,10 @@ def philox_4x32_10(counter, key):
     return [np.asarray(v, dtype=np.uint32) for v in c]
 
 
-def dropout_keep(n, p, seed, offset):
-    """Truth value of each of n elements: kept."""
+def dropout_keep(n, p, seed, offset, first=0):
+    """Truth value of each of the n elements from `first` (a multiple of 4) on: kept."""
     seed, offset = int(seed) & (2 ** 64 - 1), int(offset) & (2 ** 64 - 1)
-    block = np.arange((n + 3) // 4, dtype=np.uint64)
+    block = np.arange((n + 3) // 4, dtype=np.uint64) + np.uint64(first // 4)
     zero = np.zeros_like(block)
     words = philox_4x32_10(
         [block & np.uint64(0xFFFFFFFF), block >> np.uint64(32),

@@ -255,6 +255,18 @@ def test_dropout_masks_non_finite_and_drops_all():
     assert torch.equal(ops.dropout_add_forward(x, res, 1.0 - 1e-12, rng), res)
 
 
+def test_dropout_beyond_32_bits():
+    # more elements than one launch covers: the mask's counter goes on across them
+    n = (1 << 34) + (1 << 33) + 4099
+    rng = torch.tensor([7, 8], device="cuda")
+    x = torch.ones((1, n), dtype=torch.bfloat16, device="cuda")
+    out = ops.dropout_add_forward(x, None, 0.5, rng)
+    for first in (0, (1 << 33) - 4096, (1 << 34) - 4096, 3 * (1 << 33) - 4096, n - 8195):
+        m = min(8192, n - first)
+        keep = torch.from_numpy(O.dropout_keep(m, 0.5, 7, 8, first)).cuda()
+        assert torch.equal(out[0, first:first + m], torch.where(keep, 2.0, 0.0).bfloat16())
+
+
 def test_dropout_gradients_and_changed_rng():
     g = gen(9)
     x = randn(g, 40, 96, dtype=torch.float32).requires_grad_(True)
