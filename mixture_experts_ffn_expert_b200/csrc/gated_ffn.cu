@@ -268,6 +268,17 @@ int check_rows(const void* p, int64_t T, int64_t cols, int64_t ld, const char* w
 
 }  // namespace
 
+namespace moe {
+int ops_device(OpsDevice* out) {
+  DeviceInfo* d;
+  if (int s = device_info(&d)) return s;
+  out->index = static_cast<int>(d - g_devices);
+  out->sms = d->sms;
+  out->status = d->status;
+  return MOE_OK;
+}
+}  // namespace moe
+
 extern "C" {
 
 size_t moe_gated_ffn_workspace_bytes(int64_t T, int64_t d, int64_t f, int backward) {

@@ -368,6 +368,629 @@ __global__ void __launch_bounds__(256) norm_backward_long_sum_kernel(const NormP
   if (!P.rms) out[P.cols + c] = db;
 }
 
+// ------------------------------------------------------------------ tile kernels
+// Many rows: one persistent block an SM walks its share of the rows in tiles of 1 to 8
+// rows, as a pipeline of warps over a ring of shared-memory slots:
+//   one thread brings tiles in with bulk copies (cp.async.bulk), as far ahead as there are
+//     slots, so that the loads in flight depend neither on registers nor on occupancy;
+//   8 row warps sum what a row needs along it (8 / rows warps a row; a lane holds many
+//     elements, so shuffles are few);
+//   the column warps merge those sums, keep their columns' weights, and in the backward
+//     pass their gradients, in registers over all rows, and write the output.
+// Barriers of the ring order them tile by tile (full, summed, free); there is no block-wide
+// barrier, so no part waits for another's latency. (With the row spread over a block and
+// two block reductions a row, 8192 x 2048 bf16 took 36 us forward; with tiles worked first
+// along rows and then along columns by all warps, 18.)
+//
+// VEC = 16 bytes of elements: rows start on 16-byte boundaries. VEC = 1: contiguous rows of
+// any width; a tile is then one run of bytes that is copied from the 16-byte boundary at or
+// before it, and its elements are read one by one.
+constexpr int kRowWarps = 8;
+constexpr int kTileMaxSlots = 8;
+constexpr int tile_threads(int column_warps) { return (kRowWarps + column_warps + 1) * 32; }
+
+struct NormTile {
+  int rows;                // a tile: 1, 2, 4 or 8
+  int slots;
+  int group;               // column threads that cover the columns once
+  int contiguous;          // rows follow one another: one copy a tile
+  uint32_t slot_bytes;     // of one matrix
+  uint32_t weight_bytes;   // backward: the weight staged in front of the ring
+};
+
+struct TileShared {
+  uint64_t full[kTileMaxSlots], summed[kTileMaxSlots], free[kTileMaxSlots];
+  float2 part[kTileMaxSlots][kRowWarps];
+  int abort;
+};
+
+// Wait for a phase of a ring barrier, suspended in the hardware for up to 0.1 ms a try (25
+// warps that poll would take the issue slots of those that work). A wait that gives up
+// (2 s) marks the block; what follows is garbage in bounds, reported through the status
+// word.
+__device__ __forceinline__ void tile_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                          int* status) {
+  const uint32_t addr = smem_u32(bar);
+  uint64_t t0 = 0;
+  for (;;) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.b32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(addr), "r"(parity), "r"(100000u)
+        : "memory");
+    if (ok || *abort) return;
+    const uint64_t now = global_timer_ns();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > kWaitLimitNs) {
+      *abort = 1;
+      atomicExch(status, 6);          // MOE_DEVICE_TIMEOUT
+      return;
+    }
+  }
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+          "r"(dst),
+      "l"(__cvta_generic_to_global(src)), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+// Bytes a tile's first row lies past the start of its slot.
+template <typename T, int VEC>
+__device__ __forceinline__ uint32_t tile_shift(const NormParams& P, long long row) {
+  return VEC == 1 ? static_cast<uint32_t>(row * P.cols * sizeof(T)) & 15u : 0u;
+}
+
+// Copies of one matrix's rows [row, row + n) into a slot; returns the bytes that will be
+// counted on `bar`. One thread. VEC == 1: the run of bytes is widened to 16-byte
+// boundaries, inside the matrix; what lies past the last boundary at its very end (fewer
+// than 16 bytes) is copied by hand, before this thread's arrival on the barrier.
+template <typename T, int VEC, bool ISSUE>
+__device__ __forceinline__ uint32_t tile_copy(const NormParams& P, const NormTile& L,
+                                              const void* base, long long ld, long long row, int n,
+                                              uint8_t* slot, uint32_t bar) {
+  const uint32_t row_bytes = static_cast<uint32_t>(P.cols) * sizeof(T);
+  if (VEC == 1) {
+    const unsigned long long b0 = static_cast<unsigned long long>(row) * row_bytes;
+    const unsigned long long b1 = b0 + static_cast<unsigned long long>(n) * row_bytes;
+    const unsigned long long all = static_cast<unsigned long long>(P.rows) * row_bytes;
+    const unsigned long long from = b0 & ~15ull;
+    const unsigned long long up = (b1 + 15) & ~15ull, last = all & ~15ull;
+    const unsigned long long to = up < last ? up : last;
+    const uint32_t bytes = to > from ? static_cast<uint32_t>(to - from) : 0u;
+    if (ISSUE) {
+      const char* src = static_cast<const char*>(base);
+      if (bytes) bulk_load(smem_u32(slot), src + from, bytes, bar);
+    } else {
+      const char* src = static_cast<const char*>(base);
+      for (unsigned long long i = to > from ? to : from; i < b1; i += sizeof(T))
+        *reinterpret_cast<T*>(slot + (i - from)) = *reinterpret_cast<const T*>(src + i);
+    }
+    return bytes;
+  }
+  if (ISSUE) {
+    const T* src = static_cast<const T*>(base) + row * ld;
+    if (L.contiguous) {
+      bulk_load(smem_u32(slot), src, n * row_bytes, bar);
+    } else {
+      for (int r = 0; r < n; ++r)
+        bulk_load(smem_u32(slot) + r * row_bytes, src + r * ld, row_bytes, bar);
+    }
+  }
+  return n * row_bytes;
+}
+
+// A thread's VEC elements as pairs of fp32 values (VEC = 1: one pair, its second value 0),
+// read from a slot by shared-memory address.
+template <int VEC>
+constexpr int pairs() {
+  return VEC == 1 ? 1 : VEC / 2;
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void ld_tile(f32x2 (&f)[pairs<VEC>()], uint32_t addr) {
+  if constexpr (VEC == 1 && sizeof(T) == 4) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+    f[0] = make2(v, 0.0f);
+  } else if constexpr (VEC == 1) {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
+    f[0] = make2(unpack2<T>(static_cast<uint32_t>(v)).x, 0.0f);
+  } else if constexpr (sizeof(T) == 4) {
+    asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
+                 : "=f"(f[0].x), "=f"(f[0].y), "=f"(f[1].x), "=f"(f[1].y)
+                 : "r"(addr));
+  } else {
+    uint32_t w[4];
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(addr));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 v = unpack2<T>(w[i]);
+      f[i] = make2(v.x, v.y);
+    }
+  }
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void st_out(T* p, const f32x2 (&f)[pairs<VEC>()]) {
+  if constexpr (VEC == 1) {
+    *p = from_f32<T>(f[0].x);
+  } else if constexpr (sizeof(T) == 4) {
+    *reinterpret_cast<float4*>(p) = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+  } else {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      w[i] = pack2<T>(f[i].x, f[i].y);
+    }
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+// VEC weights (or biases) as pairs.
+template <typename T, int VEC>
+__device__ __forceinline__ void load_weight2(f32x2 (&f)[pairs<VEC>()], const void* p, int wf32,
+                                             int col, float none) {
+  float w[VEC];
+  load_weight<T, VEC>(w, p, wf32, col, none);
+  if constexpr (VEC == 1) {
+    f[0] = make2(w[0], 0.0f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) f[i] = make2(w[2 * i], w[2 * i + 1]);
+  }
+}
+
+// This block's rows: [lo, hi).
+__device__ __forceinline__ void tile_range(const NormParams& P, long long* lo, long long* hi) {
+  *lo = P.rows * blockIdx.x / gridDim.x;
+  *hi = P.rows * (blockIdx.x + 1) / gridDim.x;
+}
+
+// a / n for a count n with its rounded reciprocal: one Newton step on the quotient gives the
+// division's result (a constant row must have exactly its value as its mean) at the cost of
+// three instructions.
+__device__ __forceinline__ float divide_by(float a, float n, float inv_n) {
+  const float q = a * inv_n;
+  return fmaf(fmaf(-q, n, a), inv_n, q);
+}
+// 1 / sqrt(v), v > 0 (or 0: infinity): the hardware's approximation, refined once.
+__device__ __forceinline__ float inv_sqrt(float v) {
+  const float y = rsqrtf(v);
+  const float e = fmaf(-0.5f * v * y, y, 0.5f);
+  return v > 1e-37f && v < 3e38f ? fmaf(y, e, y) : y;
+}
+
+// Vectors of part q of a row of n vectors that wpr warps share in rounds of 32 each.
+__device__ __forceinline__ int part_vectors(int n, int wpr, int q) {
+  const int round = wpr * 32;
+  const int rem = n % round - q * 32;
+  return n / round * 32 + min(max(rem, 0), 32);
+}
+
+// The block's part of the pipeline that brings tiles in; PLANES matrices (x, and dy) a
+// slot. One thread. Returns once every tile has landed.
+template <typename T, int VEC, int PLANES>
+__device__ __forceinline__ void tile_producer(const NormParams& P, const NormTile& L, uint8_t* ring,
+                                              TileShared& sh, long long lo, long long hi, int tiles,
+                                              int* status) {
+  int s = 0;
+  uint32_t ph = 0;
+  for (int t = 0; t < tiles; ++t) {
+    tile_wait(&sh.free[s], ph ^ 1u, &sh.abort, status);
+    const long long row = lo + static_cast<long long>(t) * L.rows;
+    const int n = static_cast<int>(hi - row < L.rows ? hi - row : L.rows);
+    uint8_t* slot = ring + static_cast<size_t>(s) * PLANES * L.slot_bytes;
+    const uint32_t bar = smem_u32(&sh.full[s]);
+    uint32_t bytes = tile_copy<T, VEC, false>(P, L, P.x, P.ldx, row, n, slot, bar);
+    if (PLANES == 2)
+      bytes += tile_copy<T, VEC, false>(P, L, P.dy, P.lddy, row, n, slot + L.slot_bytes, bar);
+    mbar_arrive_expect_tx(bar, bytes);
+    tile_copy<T, VEC, true>(P, L, P.x, P.ldx, row, n, slot, bar);
+    if (PLANES == 2)
+      tile_copy<T, VEC, true>(P, L, P.dy, P.lddy, row, n, slot + L.slot_bytes, bar);
+    if (++s == L.slots) {
+      s = 0;
+      ph ^= 1u;
+    }
+  }
+}
+
+__device__ __forceinline__ void tile_init(const NormTile& L, TileShared& sh, int column_warps) {
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < L.slots; ++s) {
+      mbar_init(smem_u32(&sh.full[s]), 1);
+      mbar_init(smem_u32(&sh.summed[s]), kRowWarps);
+      mbar_init(smem_u32(&sh.free[s]), column_warps);
+    }
+    sh.abort = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+}
+
+template <typename T, int VEC, int VPT, int CW, bool RMS>
+__global__ void __launch_bounds__(tile_threads(CW), 1)
+    norm_forward_tile_kernel(const NormParams P, const NormTile L, int* status) {
+  constexpr int kVecBytes = VEC * static_cast<int>(sizeof(T));
+  constexpr int kPairs = pairs<VEC>();
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ TileShared sh;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  tile_init(L, sh, CW);
+  pdl_wait();
+  pdl_launch_dependents();
+  long long lo, hi;
+  tile_range(P, &lo, &hi);
+  const int tiles = static_cast<int>((hi - lo + L.rows - 1) / L.rows);
+  const uint32_t row_bytes = static_cast<uint32_t>(P.cols) * sizeof(T);
+  const int n_vec = P.cols / VEC;
+  const int wpr = kRowWarps / L.rows;
+  int s = 0;
+  uint32_t ph = 0;
+  if (warp == kRowWarps + CW) {
+    if (lane == 0) tile_producer<T, VEC, 1>(P, L, ring, sh, lo, hi, tiles, status);
+  } else if (warp < kRowWarps) {
+    // ---- row warps: the sum of this warp's part of its row, and the squared differences
+    // from the part's own mean (sum (x - m)^2 = sum (x - m_w)^2 + n_w (m_w - m)^2 later)
+    const int my_row = warp / wpr, q = warp - my_row * wpr;
+    const float own_n = static_cast<float>(part_vectors(n_vec, wpr, q) * VEC);
+    const float own_inv = own_n > 0.0f ? 1.0f / own_n : 0.0f;
+    const uint32_t base = smem_u32(ring) + my_row * row_bytes + (q * 32 + lane) * kVecBytes;
+    const uint32_t step = wpr * 32 * kVecBytes;
+    // every lane reads the same number of vectors, the last perhaps beyond the row: masked
+    const int rounds = (n_vec + wpr * 32 - 1) / (wpr * 32);
+    const bool last = (rounds - 1) * wpr * 32 + q * 32 + lane < n_vec;
+    for (int t = 0; t < tiles; ++t) {
+      const long long row0 = lo + static_cast<long long>(t) * L.rows;
+      tile_wait(&sh.full[s], ph, &sh.abort, status);
+      if (row0 + my_row < hi) {
+        const uint32_t x = base + s * L.slot_bytes + tile_shift<T, VEC>(P, row0);
+        float sum = 0.0f, part_mean = 0.0f;
+        if (!RMS) {
+          f32x2 acc[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
+          auto add = [&](int k) {
+            f32x2 a[kPairs];
+            ld_tile<T, VEC>(a, x + k * step);
+#pragma unroll
+            for (int j = 0; j < kPairs; ++j) acc[j & 1] = add2(acc[j & 1], a[j]);
+          };
+#pragma unroll 4
+          for (int k = 0; k < rounds - 1; ++k) add(k);
+          if (last) add(rounds - 1);
+          const f32x2 both = add2(acc[0], acc[1]);
+          sum = warp_sum(both.x + both.y);
+          part_mean = divide_by(sum, own_n, own_inv);
+        }
+        const f32x2 shift = make2(-part_mean, VEC == 1 ? 0.0f : -part_mean);
+        f32x2 acc[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
+        auto add = [&](int k) {
+          f32x2 a[kPairs];
+          ld_tile<T, VEC>(a, x + k * step);
+#pragma unroll
+          for (int j = 0; j < kPairs; ++j) {
+            const f32x2 c = RMS ? a[j] : add2(a[j], shift);
+            acc[j & 1] = fma2(c, c, acc[j & 1]);
+          }
+        };
+#pragma unroll 4
+        for (int k = 0; k < rounds - 1; ++k) add(k);
+        if (last) add(rounds - 1);
+        const f32x2 both = add2(acc[0], acc[1]);
+        float sq = both.x + both.y;
+        sq = warp_sum(sq);
+        if (lane == 0) sh.part[s][warp] = make_float2(sum, sq);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sh.summed[s]));
+      if (++s == L.slots) {
+        s = 0;
+        ph ^= 1u;
+      }
+    }
+  } else {
+    // ---- column warps
+    const int ct = threadIdx.x - kRowWarps * 32;
+    const int groups = CW * 32 / L.group;
+    const int g = ct / L.group, tid = ct - g * L.group;
+    f32x2 w[VPT][kPairs], b[RMS ? 1 : VPT][kPairs];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int col = (i * L.group + tid) * VEC;
+      if (g < groups && col < P.cols) {
+        load_weight2<T, VEC>(w[i], P.weight, P.wf32, col, 1.0f);
+        if (!RMS) load_weight2<T, VEC>(b[RMS ? 0 : i], P.bias, P.wf32, col, 0.0f);
+      }
+    }
+    const float n = static_cast<float>(P.cols), inv_n = 1.0f / n;
+    const int l = lane & 7;           // lane l (mod 8) merges what row warp l summed
+    const float part_n = static_cast<float>(part_vectors(n_vec, wpr, l % wpr) * VEC);
+    const float part_inv = part_n > 0.0f ? 1.0f / part_n : 0.0f;
+    for (int t = 0; t < tiles; ++t) {
+      const long long row0 = lo + static_cast<long long>(t) * L.rows;
+      const int valid = static_cast<int>(hi - row0 < L.rows ? hi - row0 : L.rows);
+      tile_wait(&sh.full[s], ph, &sh.abort, status);
+      tile_wait(&sh.summed[s], ph, &sh.abort, status);
+      // the rows' statistics, all rows at once over the lanes
+      const float2 p = l / wpr < valid ? sh.part[s][l] : make_float2(0.0f, 0.0f);
+      float mean = 0.0f, m2 = p.y;
+      if (!RMS) {
+        float total = p.x;
+        for (int o = 1; o < wpr; o <<= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+        mean = divide_by(total, n, inv_n);
+        const float d = divide_by(p.x, part_n, part_inv) - mean;
+        m2 += part_n * d * d;
+      }
+      for (int o = 1; o < wpr; o <<= 1) m2 += __shfl_xor_sync(0xffffffffu, m2, o);
+      const float rstd = inv_sqrt(fmaf(m2, inv_n, P.eps));
+      if (warp == kRowWarps && lane < 8 && l % wpr == 0 && l / wpr < valid) {
+        if (!RMS && P.mean) P.mean[row0 + l / wpr] = mean;
+        if (P.rstd) P.rstd[row0 + l / wpr] = rstd;
+      }
+      uint32_t x = smem_u32(ring) + s * L.slot_bytes + tile_shift<T, VEC>(P, row0) +
+                   g * row_bytes + tid * kVecBytes;
+      T* y = static_cast<T*>(P.y) + (row0 + g) * P.ldy + tid * VEC;
+#pragma unroll 2
+      for (int r0 = 0; r0 < valid; r0 += groups, x += groups * row_bytes, y += groups * P.ldy) {
+        const int r = r0 + g;
+        const float row_mean = RMS ? 0.0f : __shfl_sync(0xffffffffu, mean, r * wpr);
+        const float row_rstd = __shfl_sync(0xffffffffu, rstd, r * wpr);
+        if (g < groups && r < valid) {
+          const f32x2 shift = make2(-row_mean, -row_mean), scale = make2(row_rstd, row_rstd);
+#pragma unroll
+          for (int i = 0; i < VPT; ++i) {
+            const int col = (i * L.group + tid) * VEC;
+            if (col < P.cols) {
+              f32x2 a[kPairs];
+              ld_tile<T, VEC>(a, x + i * L.group * kVecBytes);
+#pragma unroll
+              for (int j = 0; j < kPairs; ++j) {
+                const f32x2 xh = mul2(RMS ? a[j] : add2(a[j], shift), scale);
+                a[j] = RMS ? mul2(xh, w[i][j]) : fma2(xh, w[i][j], b[RMS ? 0 : i][j]);
+              }
+              st_out<T, VEC>(y + i * L.group * VEC, a);
+            }
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sh.free[s]));
+      if (++s == L.slots) {
+        s = 0;
+        ph ^= 1u;
+      }
+    }
+  }
+}
+
+template <typename T, int VEC, int VPT, int CW, bool RMS, bool GRADW>
+__global__ void __launch_bounds__(tile_threads(CW), 1)
+    norm_backward_tile_kernel(const NormParams P, const NormTile L, int* status) {
+  constexpr bool kHold = VPT * VEC <= 8;           // column warps: weights in registers
+  constexpr int kVecBytes = VEC * static_cast<int>(sizeof(T));
+  constexpr int kPairs = pairs<VEC>();
+  extern __shared__ __align__(128) uint8_t smem_tile[];
+  __shared__ TileShared sh;
+  uint8_t* ring = smem_tile + L.weight_bytes;
+  float* ws = reinterpret_cast<float*>(smem_tile);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  tile_init(L, sh, CW);
+  pdl_wait();
+  pdl_launch_dependents();
+  long long lo, hi;
+  tile_range(P, &lo, &hi);
+  const int tiles = static_cast<int>((hi - lo + L.rows - 1) / L.rows);
+  // the weight in shared memory, fp32; the first tiles are on their way meanwhile
+  if (warp < kRowWarps + CW) {
+    for (int c = threadIdx.x; c < P.cols; c += (kRowWarps + CW) * 32) {
+      float v[1];
+      load_weight<T, 1>(v, P.weight, P.wf32, c, 1.0f);
+      ws[c] = v[0];
+    }
+    asm volatile("bar.sync 1, %0;" ::"n"((kRowWarps + CW) * 32) : "memory");
+  }
+  const uint32_t row_bytes = static_cast<uint32_t>(P.cols) * sizeof(T);
+  const int n_vec = P.cols / VEC;
+  const int wpr = kRowWarps / L.rows;
+  int s = 0;
+  uint32_t ph = 0;
+  if (warp == kRowWarps + CW) {
+    if (lane == 0) tile_producer<T, VEC, 2>(P, L, ring, sh, lo, hi, tiles, status);
+    return;
+  }
+  if (warp < kRowWarps) {
+    // ---- row warps: their part of the sums of g * (x - mean) and of g
+    const int my_row = warp / wpr, q = warp - my_row * wpr;
+    float next_mean = 0.0f, next_rstd = 0.0f;      // loaded one tile ahead
+    if (lo + my_row < hi) {
+      if (!RMS) next_mean = P.mean[lo + my_row];
+      next_rstd = P.rstd[lo + my_row];
+    }
+    const uint32_t base = smem_u32(ring) + my_row * row_bytes + (q * 32 + lane) * kVecBytes;
+    const uint32_t step = wpr * 32 * kVecBytes;
+    const uint32_t w_base = smem_u32(ws) + (q * 32 + lane) * (VEC * 4);
+    const int rounds = (n_vec + wpr * 32 - 1) / (wpr * 32);
+    const bool last = (rounds - 1) * wpr * 32 + q * 32 + lane < n_vec;
+    for (int t = 0; t < tiles; ++t) {
+      const long long row0 = lo + static_cast<long long>(t) * L.rows;
+      const float mean = next_mean, rstd = next_rstd;
+      if (row0 + L.rows + my_row < hi) {
+        if (!RMS) next_mean = P.mean[row0 + L.rows + my_row];
+        next_rstd = P.rstd[row0 + L.rows + my_row];
+      }
+      tile_wait(&sh.full[s], ph, &sh.abort, status);
+      if (row0 + my_row < hi) {
+        const uint32_t x = base + s * 2 * L.slot_bytes + tile_shift<T, VEC>(P, row0);
+        const f32x2 shift = make2(-mean, -mean);
+        f32x2 s1[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}}, s2[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
+        auto add = [&](int k) {
+          f32x2 a[kPairs], d[kPairs], wv[kPairs];
+          ld_tile<T, VEC>(a, x + k * step);
+          ld_tile<T, VEC>(d, x + L.slot_bytes + k * step);
+          const uint32_t wa = w_base + k * wpr * (32 * VEC * 4);
+          if constexpr (VEC == 1) {
+            ld_tile<float, 1>(wv, wa);
+          } else {
+#pragma unroll
+            for (int j = 0; j < kPairs; j += 2)
+              ld_tile<float, 4>(*reinterpret_cast<f32x2(*)[2]>(wv + j), wa + j * 8);
+          }
+#pragma unroll
+          for (int j = 0; j < kPairs; ++j) {
+            const f32x2 gy = mul2(d[j], wv[j]);
+            s2[j & 1] = fma2(gy, RMS ? a[j] : add2(a[j], shift), s2[j & 1]);
+            if (!RMS) s1[j & 1] = add2(s1[j & 1], gy);
+          }
+        };
+#pragma unroll 2
+        for (int k = 0; k < rounds - 1; ++k) add(k);
+        if (last) add(rounds - 1);
+        const f32x2 b1 = add2(s1[0], s1[1]), b2 = add2(s2[0], s2[1]);
+        float c1 = b1.x + b1.y, c2 = b2.x + b2.y;
+        c2 = warp_sum(c2) * rstd;
+        if (!RMS) c1 = warp_sum(c1);
+        if (lane == 0) sh.part[s][warp] = make_float2(c1, c2);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sh.summed[s]));
+      if (++s == L.slots) {
+        s = 0;
+        ph ^= 1u;
+      }
+    }
+    return;
+  }
+  // ---- column warps
+  const int ct = threadIdx.x - kRowWarps * 32;
+  const int groups = CW * 32 / L.group;
+  const int g = ct / L.group, tid = ct - g * L.group;
+  const uint32_t w_at = smem_u32(ws) + tid * (VEC * 4);
+  auto weights = [&](f32x2 (&f)[kPairs], int i) {
+    const uint32_t at = w_at + i * L.group * (VEC * 4);
+    if constexpr (VEC == 1) {
+      ld_tile<float, 1>(f, at);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kPairs; j += 2)
+        ld_tile<float, 4>(*reinterpret_cast<f32x2(*)[2]>(f + j), at + j * 8);
+    }
+  };
+  f32x2 w[kHold ? VPT : 1][kPairs], dw[GRADW ? VPT : 1][kPairs],
+      db[GRADW && !RMS ? VPT : 1][kPairs];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    if (kHold && (i * L.group + tid) * VEC < P.cols) weights(w[kHold ? i : 0], i);
+#pragma unroll
+    for (int j = 0; j < kPairs; ++j) {
+      if (GRADW) dw[GRADW ? i : 0][j] = make2(0.0f, 0.0f);
+      if (GRADW && !RMS) db[GRADW && !RMS ? i : 0][j] = make2(0.0f, 0.0f);
+    }
+  }
+  const float inv = 1.0f / static_cast<float>(P.cols);
+  const int l = lane & 7;
+  // lane l holds the statistics of row l of the tile, loaded one tile ahead
+  float next_mean = 0.0f, next_rstd = 0.0f;
+  auto load_stats = [&](long long row) {
+    if (l < L.rows && row + l < hi) {
+      if (!RMS) next_mean = P.mean[row + l];
+      next_rstd = P.rstd[row + l];
+    }
+  };
+  load_stats(lo);
+  for (int t = 0; t < tiles; ++t) {
+    const long long row0 = lo + static_cast<long long>(t) * L.rows;
+    const int valid = static_cast<int>(hi - row0 < L.rows ? hi - row0 : L.rows);
+    const float mean = next_mean, rstd = next_rstd;
+    load_stats(row0 + L.rows);
+    tile_wait(&sh.full[s], ph, &sh.abort, status);
+    tile_wait(&sh.summed[s], ph, &sh.abort, status);
+    const float2 p = l / wpr < valid ? sh.part[s][l] : make_float2(0.0f, 0.0f);
+    float c1 = p.x, c2 = p.y;
+    for (int o = 1; o < wpr; o <<= 1) {
+      c2 += __shfl_xor_sync(0xffffffffu, c2, o);
+      if (!RMS) c1 += __shfl_xor_sync(0xffffffffu, c1, o);
+    }
+    c1 *= inv;
+    c2 *= inv;
+    uint32_t x = smem_u32(ring) + s * 2 * L.slot_bytes + tile_shift<T, VEC>(P, row0) +
+                 g * row_bytes + tid * kVecBytes;
+    T* dx = static_cast<T*>(P.y) + (row0 + g) * P.ldy + tid * VEC;
+    for (int r0 = 0; r0 < valid; r0 += groups, x += groups * row_bytes, dx += groups * P.ldy) {
+      const int r = r0 + g;
+      const float row_mean = RMS ? 0.0f : __shfl_sync(0xffffffffu, mean, r);
+      const float row_rstd = __shfl_sync(0xffffffffu, rstd, r);
+      const float row_c2 = __shfl_sync(0xffffffffu, c2, r * wpr);
+      const float row_c1 = RMS ? 0.0f : __shfl_sync(0xffffffffu, c1, r * wpr);
+      if (g < groups && r < valid) {
+        const f32x2 shift = make2(-row_mean, -row_mean), scale = make2(row_rstd, row_rstd);
+        const f32x2 minus_c1 = make2(-row_c1, -row_c1), minus_c2 = make2(-row_c2, -row_c2);
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+          const int col = (i * L.group + tid) * VEC;
+          if (col < P.cols) {
+            f32x2 a[kPairs], d[kPairs];
+            ld_tile<T, VEC>(a, x + i * L.group * kVecBytes);
+            ld_tile<T, VEC>(d, x + L.slot_bytes + i * L.group * kVecBytes);
+            if (!kHold) weights(w[0], i);
+#pragma unroll
+            for (int j = 0; j < kPairs; ++j) {
+              const f32x2 xh = mul2(RMS ? a[j] : add2(a[j], shift), scale);
+              if (GRADW) dw[GRADW ? i : 0][j] = fma2(d[j], xh, dw[GRADW ? i : 0][j]);
+              if (GRADW && !RMS) db[GRADW && !RMS ? i : 0][j] = add2(db[GRADW && !RMS ? i : 0][j], d[j]);
+              const f32x2 gc = RMS ? mul2(d[j], w[kHold ? i : 0][j])
+                                   : fma2(d[j], w[kHold ? i : 0][j], minus_c1);
+              a[j] = mul2(scale, fma2(xh, minus_c2, gc));
+            }
+            if (P.y) st_out<T, VEC>(dx + i * L.group * VEC, a);
+          }
+        }
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&sh.free[s]));
+    if (++s == L.slots) {
+      s = 0;
+      ph ^= 1u;
+    }
+  }
+  if (!GRADW) return;
+  // The groups add their sums in order in shared memory (the ring is free: the column warps
+  // have read every tile), and the last writes the block's partial row.
+  asm volatile("bar.sync 2, %0;" ::"n"(CW * 32) : "memory");
+  float* acc = reinterpret_cast<float*>(ring);
+  float* out = P.partial + static_cast<size_t>(blockIdx.x) * (RMS ? 1 : 2) * P.cols;
+  for (int k = 0; k < groups; ++k) {
+    if (g == k) {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int col = (i * L.group + tid) * VEC;
+        if (col < P.cols) {
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) {
+            const float2 pw = dw[GRADW ? i : 0][j / 2];
+            const float2 pb = RMS ? make_float2(0.0f, 0.0f) : db[GRADW && !RMS ? i : 0][j / 2];
+            float p = j & 1 ? pw.y : pw.x;
+            float q2 = j & 1 ? pb.y : pb.x;
+            if (k > 0) {
+              p += acc[col + j];
+              if (!RMS) q2 += acc[P.cols + col + j];
+            }
+            float* dst = k == groups - 1 ? out : acc;
+            dst[col + j] = p;
+            if (!RMS) dst[P.cols + col + j] = q2;
+          }
+        }
+      }
+    }
+    asm volatile("bar.sync 2, %0;" ::"n"(CW * 32) : "memory");
+  }
+}
+
 // Sum of the blocks' partial rows: 32 columns a block, 16 threads a column that each walk
 // every 16th partial row, added in a fixed order. blockIdx.y picks dweight or dbias.
 template <typename W>

@@ -3,6 +3,7 @@
 // synchronises the host or allocates device memory.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstdio>
@@ -56,19 +57,97 @@ cudaError_t launch_norm_forward(const moe::NormParams& P, int group, cudaStream_
                            dim3(group * per_block), 0, st, 1, P, group);
 }
 
+// Tile kernels: enough rows that every SM has several (600 x 7168 bf16 forward: 8.0 us, 9.6
+// with a block a row).
+constexpr int64_t kTileMinRows = 592;
+constexpr size_t kTileSmem = 208 * 1024;
+// 16 column warps beside the 8 row warps (with 8, 4096 x 7168 bf16 forward took 36 us
+// instead of 26 and the backward pass up to 30% longer).
+constexpr int kColumnWarps = 16;
+
+// Rows a tile and slots, for `planes` matrices (x, and dy in the backward pass): three
+// tiles of as many rows as fit, more tiles when they are small.
+bool tile_shape(moe::NormTile* L, const moe::NormParams& P, int vec, int vpt, int column_warps,
+                size_t esize, int planes, bool contiguous, size_t* smem) {
+  const int n = P.cols / vec;
+  L->group = round32((n + vpt - 1) / vpt);
+  if (L->group > column_warps * 32) return false;
+  L->contiguous = contiguous;
+  L->weight_bytes = planes == 2 ? uint32_t((size_t(P.cols) * 4 + 127) / 128 * 128) : 0;
+  if (L->weight_bytes >= kTileSmem) return false;
+  const size_t room = kTileSmem - L->weight_bytes;
+  const size_t extra = vec == 1 ? 32 : 0;         // a run of bytes widened to 16-byte boundaries
+  for (int rows = moe::kRowWarps; rows >= 1; rows /= 2) {
+    const size_t slot = (size_t(P.cols) * esize * rows + extra + 127) / 128 * 128;
+    const size_t tile = slot * planes;
+    if (tile * 3 > room && !(rows == 1 && tile * 2 <= room)) continue;
+    size_t slots = room / tile;
+    if (slots > moe::kTileMaxSlots) slots = moe::kTileMaxSlots;
+    L->rows = rows;
+    L->slots = int(slots);
+    L->slot_bytes = uint32_t(slot);
+    *smem = L->weight_bytes + tile * slots;
+    return true;
+  }
+  return false;
+}
+
+// Raise a tile kernel's shared-memory limit, once a device (`done`: the kernel's own bits).
+template <typename K>
+cudaError_t tile_attribute(K kernel, std::atomic<uint64_t>* done, int device) {
+  const uint64_t bit = 1ull << device;
+  if (done->load(std::memory_order_acquire) & bit) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(
+      kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kTileSmem));
+  if (e == cudaSuccess) done->fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
+template <typename T, int VEC, int VPT, bool RMS>
+cudaError_t launch_norm_forward_tile(const moe::NormParams& P, const moe::NormTile& L, size_t smem,
+                                     const moe::OpsDevice& d, cudaStream_t st) {
+  static std::atomic<uint64_t> done{0};
+  const auto kernel = moe::norm_forward_tile_kernel<T, VEC, VPT, kColumnWarps, RMS>;
+  const cudaError_t e = tile_attribute(kernel, &done, d.index);
+  if (e != cudaSuccess) return e;
+  return launch_overlapped(kernel, dim3(d.sms), dim3(moe::tile_threads(kColumnWarps)), smem, st, 1, P, L,
+                           d.status);
+}
+
+// Runs the tile kernel with the fewest vectors a column thread that cover the columns; false
+// when none does.
+template <typename T, int VEC, bool RMS, int VPT, int MAX>
+bool norm_forward_tile(const moe::NormParams& P, bool contiguous, const moe::OpsDevice& d,
+                       cudaStream_t st, cudaError_t* e) {
+  moe::NormTile L;
+  size_t smem;
+  if (tile_shape(&L, P, VEC, VPT, kColumnWarps, sizeof(T), 1, contiguous, &smem)) {
+    *e = launch_norm_forward_tile<T, VEC, VPT, RMS>(P, L, smem, d, st);
+    return true;
+  }
+  if constexpr (VPT < MAX) return norm_forward_tile<T, VEC, RMS, VPT * 2, MAX>(P, contiguous, d, st, e);
+  return false;
+}
+
 template <typename T>
-cudaError_t norm_forward_any(const moe::NormParams& P, bool vec, cudaStream_t st) {
+cudaError_t norm_forward_any(const moe::NormParams& P, bool vec, bool contiguous,
+                             const moe::OpsDevice& d, cudaStream_t st) {
   constexpr int V = 16 / sizeof(T);
-  // Few rows: as many threads a row as it has vectors (latency). Many rows: several
-  // vectors a thread, short rows a warp each (no block barrier in the statistics).
-  const bool few = P.rows < 592;
+  // Few rows: as many threads a row as it has vectors (latency). Many unaligned rows that
+  // are not contiguous: short ones a warp each, no block barrier in the statistics.
+  const bool few = P.rows < kTileMinRows;
+  if (!few && (vec || contiguous)) {
+    cudaError_t e;
+    if (vec ? (P.rms ? norm_forward_tile<T, V, true, 1, 4>(P, contiguous, d, st, &e)
+                     : norm_forward_tile<T, V, false, 1, 4>(P, contiguous, d, st, &e))
+            : (P.rms ? norm_forward_tile<T, 1, true, 4, 32>(P, contiguous, d, st, &e)
+                     : norm_forward_tile<T, 1, false, 4, 32>(P, contiguous, d, st, &e)))
+      return e;
+  }
   if (vec) {
     const int n = P.cols / V;
     if (n <= 32) return launch_norm_forward<T, V, 1>(P, 32, st);
-    if (!few && n <= 64) return launch_norm_forward<T, V, 2>(P, 32, st);
-    if (!few && n <= 128) return launch_norm_forward<T, V, 4>(P, 32, st);
-    if (!few && n <= 256) return launch_norm_forward<T, V, 8>(P, 32, st);
-    if (few && n <= 1024) return launch_norm_forward<T, V, 1>(P, round32(n), st);
+    if (n <= 1024) return launch_norm_forward<T, V, 1>(P, round32(n), st);
     if (n <= 2048) return launch_norm_forward<T, V, 4>(P, round32((n + 3) / 4), st);
     if (n <= 8192) return launch_norm_forward<T, V, 8>(P, round32((n + 7) / 8), st);
   } else {
@@ -99,9 +178,45 @@ cudaError_t launch_norm_backward(const moe::NormParams& P, int group, int* block
                            dim3(group * groups), smem, st, 1, P, group);
 }
 
+template <typename T, int VEC, int VPT, bool RMS, bool GRADW>
+cudaError_t launch_norm_backward_tile(const moe::NormParams& P, const moe::NormTile& L, size_t smem,
+                                      const moe::OpsDevice& d, int* blocks, cudaStream_t st) {
+  static std::atomic<uint64_t> done{0};
+  const auto kernel = moe::norm_backward_tile_kernel<T, VEC, VPT, kColumnWarps, RMS, GRADW>;
+  const cudaError_t e = tile_attribute(kernel, &done, d.index);
+  if (e != cudaSuccess) return e;
+  *blocks = d.sms < kNormBlocks ? d.sms : kNormBlocks;
+  return launch_overlapped(kernel, dim3(*blocks), dim3(moe::tile_threads(kColumnWarps)), smem, st, 1, P, L,
+                           d.status);
+}
+
+template <typename T, int VEC, bool RMS, bool GRADW, int VPT, int MAX>
+bool norm_backward_tile(const moe::NormParams& P, bool contiguous, const moe::OpsDevice& d,
+                        int* blocks, cudaStream_t st, cudaError_t* e) {
+  moe::NormTile L;
+  size_t smem;
+  if (tile_shape(&L, P, VEC, VPT, kColumnWarps, sizeof(T), 2, contiguous, &smem)) {
+    // the groups' sums meet in the ring: two planes of fp32 columns
+    const bool meet = kColumnWarps * 32 / L.group > 1;
+    if (meet && smem - L.weight_bytes < size_t(P.cols) * 8) return false;
+    *e = launch_norm_backward_tile<T, VEC, VPT, RMS, GRADW>(P, L, smem, d, blocks, st);
+    return true;
+  }
+  if constexpr (VPT < MAX)
+    return norm_backward_tile<T, VEC, RMS, GRADW, VPT * 2, MAX>(P, contiguous, d, blocks, st, e);
+  return false;
+}
+
 template <typename T, bool RMS, bool GRADW>
-cudaError_t norm_backward_any(const moe::NormParams& P, bool vec, int* blocks, cudaStream_t st) {
+cudaError_t norm_backward_any(const moe::NormParams& P, bool vec, bool contiguous,
+                              const moe::OpsDevice& d, int* blocks, cudaStream_t st) {
   constexpr int V = 16 / sizeof(T);
+  if (P.rows >= kTileMinRows && (vec || contiguous)) {
+    cudaError_t e;
+    if (vec ? norm_backward_tile<T, V, RMS, GRADW, 1, 4>(P, contiguous, d, blocks, st, &e)
+            : norm_backward_tile<T, 1, RMS, GRADW, 4, 32>(P, contiguous, d, blocks, st, &e))
+      return e;
+  }
   if (vec) {
     const int n = P.cols / V;
     if (n <= 1024) return launch_norm_backward<T, V, 1, RMS, GRADW>(P, round32(n), blocks, st);
@@ -131,13 +246,13 @@ cudaError_t norm_backward_any(const moe::NormParams& P, bool vec, int* blocks, c
 }
 
 template <typename T>
-cudaError_t norm_backward_typed(const moe::NormParams& P, bool vec, bool gradw, int* blocks,
-                                cudaStream_t st) {
+cudaError_t norm_backward_typed(const moe::NormParams& P, bool vec, bool contiguous, bool gradw,
+                                const moe::OpsDevice& d, int* blocks, cudaStream_t st) {
   if (P.rms)
-    return gradw ? norm_backward_any<T, true, true>(P, vec, blocks, st)
-                 : norm_backward_any<T, true, false>(P, vec, blocks, st);
-  return gradw ? norm_backward_any<T, false, true>(P, vec, blocks, st)
-               : norm_backward_any<T, false, false>(P, vec, blocks, st);
+    return gradw ? norm_backward_any<T, true, true>(P, vec, contiguous, d, blocks, st)
+                 : norm_backward_any<T, true, false>(P, vec, contiguous, d, blocks, st);
+  return gradw ? norm_backward_any<T, false, true>(P, vec, contiguous, d, blocks, st)
+               : norm_backward_any<T, false, false>(P, vec, contiguous, d, blocks, st);
 }
 
 // Whether rows of this tensor can be read as 16-byte vectors.
@@ -282,10 +397,15 @@ int moe_norm_forward(int kind, int dtype, int wdtype, int64_t rows, int64_t cols
   P.wf32 = wdtype == MOE_DTYPE_FP32;
   const bool vec = cols % (16 / es) == 0 && vector_rows(x, rows, ldx, es) &&
                    vector_rows(y, rows, ldy, es) && aligned(weight, 16) && aligned(bias, 16);
+  const bool contiguous = ldx == cols && aligned(x, 16);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = dtype == MOE_DTYPE_BF16   ? norm_forward_any<__nv_bfloat16>(P, vec, st)
-                        : dtype == MOE_DTYPE_FP16 ? norm_forward_any<__half>(P, vec, st)
-                                                  : norm_forward_any<float>(P, vec, st);
+  moe::OpsDevice d;
+  if (int s = moe::ops_device(&d)) return s;
+  const cudaError_t e = dtype == MOE_DTYPE_BF16
+                            ? norm_forward_any<__nv_bfloat16>(P, vec, contiguous, d, st)
+                        : dtype == MOE_DTYPE_FP16
+                            ? norm_forward_any<__half>(P, vec, contiguous, d, st)
+                            : norm_forward_any<float>(P, vec, contiguous, d, st);
   return launch_status(e, "norm forward");
 }
 
@@ -346,12 +466,15 @@ int moe_norm_backward(int kind, int dtype, int wdtype, int64_t rows, int64_t col
   const bool vec = cols % (16 / es) == 0 && vector_rows(x, rows, ldx, es) &&
                    vector_rows(dy, rows, lddy, es) && (!dx || vector_rows(dx, rows, lddx, es)) &&
                    aligned(weight, 16);
+  const bool contiguous = ldx == cols && lddy == cols && aligned(x, 16) && aligned(dy, 16);
   int blocks = 0;
+  moe::OpsDevice d;
+  if (int s = moe::ops_device(&d)) return s;
   cudaError_t e = dtype == MOE_DTYPE_BF16
-                      ? norm_backward_typed<__nv_bfloat16>(P, vec, gradw, &blocks, st)
+                      ? norm_backward_typed<__nv_bfloat16>(P, vec, contiguous, gradw, d, &blocks, st)
                   : dtype == MOE_DTYPE_FP16
-                      ? norm_backward_typed<__half>(P, vec, gradw, &blocks, st)
-                      : norm_backward_typed<float>(P, vec, gradw, &blocks, st);
+                      ? norm_backward_typed<__half>(P, vec, contiguous, gradw, d, &blocks, st)
+                      : norm_backward_typed<float>(P, vec, contiguous, gradw, d, &blocks, st);
   if (e == cudaSuccess && gradw) {
     const dim3 grid(unsigned((cols + 31) / 32), dbias ? 2 : 1);
     const int planes = P.rms ? 1 : 2;

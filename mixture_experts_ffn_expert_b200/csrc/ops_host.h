@@ -18,6 +18,14 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 EncodeTiledFn tensor_map_encoder();
 
+// The current device, its SM count and its status word (device memory); checks that it is
+// an sm_100 device with an index below 64. MOE_OK or a recorded failure.
+struct OpsDevice {
+  int index, sms;
+  int* status;
+};
+int ops_device(OpsDevice* out);
+
 // Launch with programmatic stream serialisation, optionally as clusters of `cluster` CTAs:
 // the kernel may start its prologue while its predecessor in the stream finishes, and
 // waits (griddepcontrol.wait) before it touches global memory.

@@ -86,7 +86,8 @@ def norm_bounds(x, w, b, dy, dtype, wdtype, kind, eps):
 
 SHAPES = [(1, 1), (3, 7), (1, 7168), (5, 32), (33, 33), (600, 128), (601, 129), (37, 1003),
           (700, 250), (64, 2048), (593, 2048), (9, 4100), (21, 7168), (7, 8200), (5, 16384),
-          (3, 16385), (4, 33000), (2, 70000), (1777, 96)]
+          (3, 16385), (4, 33000), (2, 70000), (1777, 96), (1300, 512), (1185, 1032),
+          (1200, 2056), (1190, 7168), (1184, 8200), (1500, 4096), (1184, 16384)]
 
 
 @pytest.mark.parametrize("kind", ["layer", "rms"])
@@ -157,6 +158,56 @@ def test_norm_strides(variant, dtype):
     # a weight that starts at an odd element
     w2 = torch.cat([w[:1], w])[1:]
     close(ops.norm_forward(x, w2), *want[0], "y with an odd weight")
+
+
+@pytest.mark.parametrize("variant", ["padded", "odd"])
+@pytest.mark.parametrize("cols", [40, 300, 1000])
+def test_norm_strides_many_rows(variant, cols):
+    g = gen(14 + cols)
+    x, dy = randn(g, 700, cols), randn(g, 700, cols)
+    w = randn(g, cols, shift=1.0)
+    want = norm_bounds(f64(x), f64(w), None, f64(dy), torch.bfloat16, torch.bfloat16, "layer", 1e-5)
+    xv, dyv = strided_variants(x)[variant], strided_variants(dy)[variant]
+    y, mean, rstd = ops.norm_forward(xv, w, save=True)
+    dx, dw, _ = ops.norm_backward(dyv, xv, w, mean, rstd)
+    for name, got, (ref, tol) in zip(("y", "dx", "dweight"), (y, dx, dw), want):
+        close(got, ref, tol, name)
+
+
+def test_norm_at_the_end_of_an_odd_matrix():
+    # the last bytes of a contiguous matrix whose size is no multiple of 16 bytes: nothing
+    # behind it is read into the result, nothing behind the output is written
+    rows, cols = 1201, 333
+    g = gen(15)
+    buf = torch.full((rows * cols + 64,), float("nan"), dtype=torch.bfloat16, device="cuda")
+    x = buf[:rows * cols].view(rows, cols)
+    x.copy_(randn(g, rows, cols))
+    out = torch.full((rows * cols + 64,), 7.0, dtype=torch.bfloat16, device="cuda")
+    lib = load_library()
+    assert lib.moe_norm_forward(0, 0, 0, rows, cols, x.data_ptr(), cols, None, None, 1e-5,
+                                out.data_ptr(), cols, None, None,
+                                torch.cuda.current_stream().cuda_stream) == 0
+    want = norm_bounds(f64(x), None, None, None, torch.bfloat16, torch.bfloat16, "layer", 1e-5)
+    close(out[:rows * cols].view(rows, cols), *want[0], "y")
+    assert torch.equal(out[rows * cols:], torch.full_like(out[rows * cols:], 7.0))
+
+
+def test_norm_in_place():
+    # y over x, and dx over dy, as the C interface allows
+    lib = load_library()
+    stream = torch.cuda.current_stream().cuda_stream
+    for rows, cols in ((5, 520), (700, 520), (700, 333), (3, 70000)):
+        g = gen(16)
+        x, dy = randn(g, rows, cols), randn(g, rows, cols)
+        y, mean, rstd = ops.norm_forward(x, save=True)
+        dx = ops.norm_backward(dy, x, None, mean, rstd)[0]
+        x2, dy2 = x.clone(), dy.clone()
+        assert lib.moe_norm_backward(0, 0, 0, rows, cols, dy2.data_ptr(), cols, x.data_ptr(), cols,
+                                     None, mean.data_ptr(), rstd.data_ptr(), dy2.data_ptr(), cols,
+                                     None, None, None, 0, stream) == 0
+        assert lib.moe_norm_forward(0, 0, 0, rows, cols, x2.data_ptr(), cols, None, None, 1e-5,
+                                    x2.data_ptr(), cols, None, None, stream) == 0
+        assert torch.equal(x2, y) and torch.equal(dy2, dx)
 
 
 def test_norm_broadcast_gradient_and_leading_dimensions():
