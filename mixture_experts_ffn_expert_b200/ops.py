@@ -15,6 +15,7 @@ Wrong shapes, types, strides or devices raise ``MoEError``; there is no fallback
 """
 from __future__ import annotations
 
+from functools import lru_cache
 from typing import Optional, Tuple
 
 import torch
@@ -47,10 +48,11 @@ def _code(table, key, what: str) -> int:
         raise _bad(f"unsupported {what} {key!r}") from None
 
 
-def _cuda(x: torch.Tensor, what: str) -> torch.device:
+def _cuda(x: torch.Tensor, what: str) -> int:
+    """Index of x's CUDA device."""
     if not isinstance(x, torch.Tensor) or not x.is_cuda:
         raise _bad(f"{what} must be a CUDA tensor")
-    return x.device
+    return x.get_device()
 
 
 def _as_rows(t: torch.Tensor, what: str) -> torch.Tensor:
@@ -74,32 +76,45 @@ def _like(t: torch.Tensor, x: torch.Tensor, what: str) -> torch.Tensor:
     return t
 
 
-class _on:
-    """Make the tensors' device current for a launch (no cost when it already is)."""
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
-    __slots__ = ("index", "guard")
 
-    def __init__(self, device: torch.device):
-        self.index, self.guard = device.index, None
+def _launch(index: int, name: str, *args) -> None:
+    """Call a C entry point with the tensors' device current and its current stream as the
+    last argument."""
+    lib = load_library()
+    if _current_device() == index:
+        status = getattr(lib, name)(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            status = getattr(lib, name)(*args, _raw_stream(index))
+    if status:
+        _check(lib, status)
 
-    def __enter__(self):
-        if torch.cuda.current_device() != self.index:
-            self.guard = torch.cuda.device(self.index)
-            self.guard.__enter__()
-        return torch.cuda.current_stream(self.index).cuda_stream or None
 
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _is_rows(t: torch.Tensor) -> bool:
+    """Whether t already is what the operators' outputs look like: contiguous (rows, cols)."""
+    return t.dim() == 2 and t.is_contiguous() and t.shape[1] > 0
+
+
+@lru_cache(maxsize=256)
+def _norm_workspace(kind: int, rows: int, cols: int) -> int:
+    return load_library().moe_norm_workspace_bytes(kind, rows, cols)
+
+
+@lru_cache(maxsize=256)
+def _ffn_workspace(T: int, d: int, f: int, backward: int) -> int:
+    return load_library().moe_gated_ffn_workspace_bytes(T, d, f, backward)
 
 
 # ------------------------------------------------------------------------ norm
-def _norm_vector(t, x, what):
+def _norm_vector(t, x, cols, what):
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor) or t.shape != (x.shape[-1],) or t.device != x.device \
-            or t.dtype not in (x.dtype, torch.float32):
-        raise _bad(f"{what} must be a ({x.shape[-1]},) tensor of x's type or fp32 on {x.device}")
+    if not isinstance(t, torch.Tensor) or t.dim() != 1 or t.numel() != cols or not t.is_cuda \
+            or t.get_device() != x.get_device() or t.dtype not in (x.dtype, torch.float32):
+        raise _bad(f"{what} must be a ({cols},) tensor of x's type or fp32 on {x.device}")
     return t if t.is_contiguous() else t.contiguous()
 
 
@@ -112,29 +127,25 @@ def norm_forward(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
     type or fp32 (the same of both). Returns y, or with ``save`` (y, mean, rstd) for
     ``norm_backward``: fp32, one a row, mean None for an RMS norm.
     """
-    device = _cuda(x, "x")
+    index = _cuda(x, "x")
     dt, kd = _code(_DTYPES, x.dtype, "dtype"), _code(_KINDS, kind, "norm kind")
-    x2 = _as_rows(x, "x")
-    weight, bias = _norm_vector(weight, x, "weight"), _norm_vector(bias, x, "bias")
+    x2 = x if _is_rows(x) else _as_rows(x, "x")
+    rows, cols = x2.shape
+    weight, bias = _norm_vector(weight, x, cols, "weight"), _norm_vector(bias, x, cols, "bias")
     if kd == MOE_NORM_RMS and bias is not None:
         raise _bad("an RMS norm has no bias")
     if weight is not None and bias is not None and weight.dtype != bias.dtype:
         raise _bad("weight and bias must have the same type")
     vec = weight if weight is not None else bias
     wdt = dt if vec is None else _DTYPES[vec.dtype]
-    rows, cols = x2.shape
-    y = torch.empty((rows, cols), dtype=x.dtype, device=device)
+    y = torch.empty_like(x, memory_format=torch.contiguous_format)
     mean = rstd = None
     if save:
-        rstd = torch.empty((rows,), dtype=torch.float32, device=device)
+        rstd = x.new_empty((rows,), dtype=torch.float32)
         if kd == MOE_NORM_LAYER:
-            mean = torch.empty((rows,), dtype=torch.float32, device=device)
-    lib = load_library()
-    with _on(device) as stream:
-        _check(lib, lib.moe_norm_forward(kd, dt, wdt, rows, cols, x2.data_ptr(), x2.stride(0),
-                                         _ptr(weight), _ptr(bias), eps, y.data_ptr(), cols,
-                                         _ptr(mean), _ptr(rstd), stream))
-    y = y if x.dim() == 2 else y.view(x.shape)
+            mean = x.new_empty((rows,), dtype=torch.float32)
+    _launch(index, "moe_norm_forward", kd, dt, wdt, rows, cols, x2.data_ptr(), x2.stride(0),
+            _ptr(weight), _ptr(bias), eps, y.data_ptr(), cols, _ptr(mean), _ptr(rstd))
     return (y, mean, rstd) if save else y
 
 
@@ -149,37 +160,36 @@ def norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: Optional[torch.Tens
     ``bias``; both have ``grad_dtype``, by default the weight's type (x's without a weight),
     and are summed in a fixed order.
     """
-    device = _cuda(x, "x")
+    index = _cuda(x, "x")
     dt, kd = _code(_DTYPES, x.dtype, "dtype"), _code(_KINDS, kind, "norm kind")
-    x2, dy2 = _as_rows(x, "x"), _as_rows(_like(dy, x, "dy"), "dy")
-    weight = _norm_vector(weight, x, "weight")
+    _like(dy, x, "dy")
+    x2 = x if _is_rows(x) else _as_rows(x, "x")
+    dy2 = dy if _is_rows(dy) else _as_rows(dy, "dy")
+    rows, cols = x2.shape
+    weight = _norm_vector(weight, x, cols, "weight")
     if kd == MOE_NORM_RMS and bias:
         raise _bad("an RMS norm has no bias")
-    rows, cols = x2.shape
-    for name, t in (("rstd", rstd),) + ((("mean", mean),) if kd == MOE_NORM_LAYER else ()):
-        if not isinstance(t, torch.Tensor) or t.shape != (rows,) or t.dtype != torch.float32 \
-                or t.device != device or not t.is_contiguous():
+    for name, t in (("rstd", rstd), ("mean", mean)):
+        if name == "mean" and kd == MOE_NORM_RMS:
+            continue
+        if not isinstance(t, torch.Tensor) or t.dim() != 1 or t.numel() != rows \
+                or t.dtype != torch.float32 or not t.is_cuda or t.get_device() != index \
+                or not t.is_contiguous():
             raise _bad(f"{name} must be the contiguous fp32 ({rows},) tensor of norm_forward")
     wtype = weight.dtype if weight is not None else grad_dtype or x.dtype
     if wtype not in (x.dtype, torch.float32) or grad_dtype not in (None, wtype):
         raise _bad("grad_dtype must be the weight's type, or x's type or fp32 without a weight")
-    dx = torch.empty((rows, cols), dtype=x.dtype, device=device) if need_dx else None
-    dweight = torch.empty((cols,), dtype=wtype, device=device) \
-        if need_dweight and weight is not None else None
-    dbias = torch.empty((cols,), dtype=wtype, device=device) if bias else None
-    lib = load_library()
+    dx = torch.empty_like(x, memory_format=torch.contiguous_format) if need_dx else None
+    dweight = torch.empty_like(weight) if need_dweight and weight is not None else None
+    dbias = x.new_empty((cols,), dtype=wtype) if bias else None
     ws, nbytes = None, 0
     if dweight is not None or dbias is not None:
-        nbytes = lib.moe_norm_workspace_bytes(kd, rows, cols)
-        ws = torch.empty((max(nbytes, 16),), dtype=torch.uint8, device=device)
-    with _on(device) as stream:
-        _check(lib, lib.moe_norm_backward(
-            kd, dt, _DTYPES[wtype], rows, cols, dy2.data_ptr(), dy2.stride(0), x2.data_ptr(),
-            x2.stride(0), _ptr(weight), _ptr(mean) if kd == MOE_NORM_LAYER else None,
-            rstd.data_ptr(), _ptr(dx), cols, _ptr(dweight), _ptr(dbias), _ptr(ws), nbytes,
-            stream))
-    if dx is not None and x.dim() != 2:
-        dx = dx.view(x.shape)
+        nbytes = _norm_workspace(kd, rows, cols)
+        ws = x.new_empty((max(nbytes, 16),), dtype=torch.uint8)
+    _launch(index, "moe_norm_backward", kd, dt, _DTYPES[wtype], rows, cols, dy2.data_ptr(),
+            dy2.stride(0), x2.data_ptr(), x2.stride(0), _ptr(weight),
+            _ptr(mean) if kd == MOE_NORM_LAYER else None, rstd.data_ptr(), _ptr(dx), cols,
+            _ptr(dweight), _ptr(dbias), _ptr(ws), nbytes)
     return dx, dweight, dbias
 
 
@@ -217,7 +227,7 @@ def rms_norm(x, weight=None, eps: float = 1e-5) -> torch.Tensor:
 # ------------------------------------------------------------------------ gated feed-forward
 def _ffn_rows(t: torch.Tensor, what: str) -> torch.Tensor:
     """t as (T, d) rows the tensor maps can describe: 16-byte aligned rows and base."""
-    t2 = _as_rows(t, what)
+    t2 = t if _is_rows(t) else _as_rows(t, what)
     if t2.data_ptr() % 16 or (t2.shape[0] > 1 and t2.stride(0) % 8):
         t2 = t2.clone(memory_format=torch.contiguous_format)
     return t2
@@ -228,8 +238,8 @@ def _ffn_weights(x, W1, W3, W2):
         raise _bad("x needs a last dimension d and W1 the shape (f, d)")
     d, f = x.shape[-1], W1.shape[0]
     for name, w, shape in (("W1", W1, (f, d)), ("W3", W3, (f, d)), ("W2", W2, (d, f))):
-        if not isinstance(w, torch.Tensor) or tuple(w.shape) != shape or w.dtype != x.dtype \
-                or w.device != x.device or not w.is_contiguous():
+        if not isinstance(w, torch.Tensor) or w.shape != shape or w.dtype != x.dtype \
+                or not w.is_cuda or w.get_device() != x.get_device() or not w.is_contiguous():
             raise _bad(f"{name} must be a contiguous {x.dtype} {shape} tensor on {x.device}")
     return d, f
 
@@ -242,25 +252,20 @@ def gated_ffn_forward(x: torch.Tensor, W1: torch.Tensor, W3: torch.Tensor, W2: t
     "silu" or "gelu" (tanh form). Returns out, or with ``save`` (out, gate, up): the (T, f)
     pre-activations for ``gated_ffn_backward``.
     """
-    device = _cuda(x, "x")
+    index = _cuda(x, "x")
     d, f = _ffn_weights(x, W1, W3, W2)
     dt, act = _code(_DTYPES, x.dtype, "dtype"), _code(_ACTS, activation, "activation")
     x2 = _ffn_rows(x, "x")
     T = x2.shape[0]
-    out = torch.empty((T, d), dtype=x.dtype, device=device)
+    out = torch.empty_like(x, memory_format=torch.contiguous_format)
     gate = up = None
     if save:
-        gate = torch.empty((T, f), dtype=x.dtype, device=device)
-        up = torch.empty((T, f), dtype=x.dtype, device=device)
-    lib = load_library()
-    nbytes = lib.moe_gated_ffn_workspace_bytes(T, d, f, 0)
-    ws = torch.empty((nbytes,), dtype=torch.uint8, device=device)
-    with _on(device) as stream:
-        _check(lib, lib.moe_gated_ffn_forward(
-            act, dt, T, d, f, x2.data_ptr(), x2.stride(0), W1.data_ptr(), W3.data_ptr(),
-            W2.data_ptr(), out.data_ptr(), d, _ptr(gate), _ptr(up), ws.data_ptr(), nbytes,
-            stream))
-    out = out if x.dim() == 2 else out.view(x.shape)
+        gate, up = x.new_empty((T, f)), x.new_empty((T, f))
+    nbytes = _ffn_workspace(T, d, f, 0)
+    ws = x.new_empty((nbytes,), dtype=torch.uint8)
+    _launch(index, "moe_gated_ffn_forward", act, dt, T, d, f, x2.data_ptr(), x2.stride(0),
+            W1.data_ptr(), W3.data_ptr(), W2.data_ptr(), out.data_ptr(), d, _ptr(gate), _ptr(up),
+            ws.data_ptr(), nbytes)
     return (out, gate, up) if save else out
 
 
@@ -270,29 +275,25 @@ def gated_ffn_backward(dout: torch.Tensor, x: torch.Tensor, W1: torch.Tensor, W3
                        needs: Tuple[bool, bool, bool, bool] = (True, True, True, True)):
     """Gradients (dx, dW1, dW3, dW2) of ``gated_ffn_forward`` from its saved gate and up;
     ``needs`` leaves out those not wanted (None in their place)."""
-    device = _cuda(x, "x")
+    index = _cuda(x, "x")
     d, f = _ffn_weights(x, W1, W3, W2)
     dt, act = _code(_DTYPES, x.dtype, "dtype"), _code(_ACTS, activation, "activation")
     x2, dout2 = _ffn_rows(x, "x"), _ffn_rows(_like(dout, x, "dout"), "dout")
     T = x2.shape[0]
     for name, t in (("gate", gate), ("up", up)):
         if not isinstance(t, torch.Tensor) or t.shape != (T, f) or t.dtype != x.dtype \
-                or t.device != device or not t.is_contiguous():
+                or not t.is_cuda or t.get_device() != index or not t.is_contiguous():
             raise _bad(f"{name} must be the contiguous ({T}, {f}) tensor of gated_ffn_forward")
-    dx = torch.empty((T, d), dtype=x.dtype, device=device) if needs[0] else None
+    dx = torch.empty_like(x, memory_format=torch.contiguous_format) if needs[0] else None
     dW1 = torch.empty_like(W1) if needs[1] else None
     dW3 = torch.empty_like(W3) if needs[2] else None
     dW2 = torch.empty_like(W2) if needs[3] else None
-    lib = load_library()
-    nbytes = lib.moe_gated_ffn_workspace_bytes(T, d, f, 1)
-    ws = torch.empty((nbytes,), dtype=torch.uint8, device=device)
-    with _on(device) as stream:
-        _check(lib, lib.moe_gated_ffn_backward(
-            act, dt, T, d, f, dout2.data_ptr(), dout2.stride(0), x2.data_ptr(), x2.stride(0),
-            W1.data_ptr(), W3.data_ptr(), W2.data_ptr(), gate.data_ptr(), up.data_ptr(), _ptr(dx),
-            d, _ptr(dW1), _ptr(dW3), _ptr(dW2), ws.data_ptr(), nbytes, stream))
-    if dx is not None and x.dim() != 2:
-        dx = dx.view(x.shape)
+    nbytes = _ffn_workspace(T, d, f, 1)
+    ws = x.new_empty((nbytes,), dtype=torch.uint8)
+    _launch(index, "moe_gated_ffn_backward", act, dt, T, d, f, dout2.data_ptr(), dout2.stride(0),
+            x2.data_ptr(), x2.stride(0), W1.data_ptr(), W3.data_ptr(), W2.data_ptr(),
+            gate.data_ptr(), up.data_ptr(), _ptr(dx), d, _ptr(dW1), _ptr(dW3), _ptr(dW2),
+            ws.data_ptr(), nbytes)
     return dx, dW1, dW3, dW2
 
 
@@ -320,22 +321,14 @@ def gated_ffn(x, W1, W3, W2, activation: str = "silu") -> torch.Tensor:
 
 
 # ------------------------------------------------------------------------ dropout
-def _rng_state(rng, p, device):
+def _rng_state(rng, p, x):
     if p == 0 and rng is None:
         return None
-    if not isinstance(rng, torch.Tensor) or rng.shape != (2,) or rng.device != device \
+    if not isinstance(rng, torch.Tensor) or rng.dim() != 1 or rng.numel() != 2 \
+            or not rng.is_cuda or rng.get_device() != x.get_device() \
             or rng.dtype not in (torch.int64, torch.uint64) or not rng.is_contiguous():
-        raise _bad(f"rng must be a contiguous int64 (2,) tensor (seed, offset) on {device}")
+        raise _bad(f"rng must be a contiguous int64 (2,) tensor (seed, offset) on {x.device}")
     return rng
-
-
-def _drop_rows(tensors):
-    """(rows, cols) views of same-shaped tensors; one line of all elements where every one
-    is contiguous."""
-    if all(t.is_contiguous() for t in tensors):
-        n = tensors[0].numel()
-        return [t.view(1, n) if n else t.reshape(0, 1) for t in tensors]
-    return [_as_rows(t, "input") for t in tensors]
 
 
 def dropout_add_forward(x: torch.Tensor, residual: Optional[torch.Tensor], p: float,
@@ -347,23 +340,27 @@ def dropout_add_forward(x: torch.Tensor, residual: Optional[torch.Tensor], p: fl
     element's position in x alone, is not stored, and is drawn again by the backward pass.
     Give every draw another offset; a captured graph reads rng at each replay.
     """
-    device = _cuda(x, "x")
+    index = _cuda(x, "x")
     dt = _code(_DTYPES, x.dtype, "dtype")
     if x.dim() == 0:
         raise _bad("x must have at least one dimension")
-    rng = _rng_state(rng, p, device)
-    ins = [x] if residual is None else [x, _like(residual, x, "residual")]
-    rows = _drop_rows(ins)
-    x2, r2 = rows[0], rows[1] if residual is not None else None
-    out = torch.empty(x.shape, dtype=x.dtype, device=device)
+    rng = _rng_state(rng, p, x)
+    if residual is not None:
+        _like(residual, x, "residual")
+    out = torch.empty_like(x, memory_format=torch.contiguous_format)
     if out.numel() == 0:
         return out
-    n, cols = x2.shape
-    lib = load_library()
-    with _on(device) as stream:
-        _check(lib, lib.moe_dropout_forward(
-            dt, n, cols, x2.data_ptr(), x2.stride(0), _ptr(r2), 0 if r2 is None else r2.stride(0),
-            p, _ptr(rng), out.data_ptr(), cols, stream))
+    if x.is_contiguous() and (residual is None or residual.is_contiguous()):
+        # one line of all elements, whatever the shape
+        n, cols = 1, x.numel()
+        x2, r2, ldx, ldr = x, residual, cols, cols
+    else:
+        x2 = _as_rows(x, "x")
+        r2 = None if residual is None else _as_rows(residual, "residual")
+        n, cols = x2.shape
+        ldx, ldr = x2.stride(0), 0 if r2 is None else r2.stride(0)
+    _launch(index, "moe_dropout_forward", dt, n, cols, x2.data_ptr(), ldx, _ptr(r2), ldr, p,
+            _ptr(rng), out.data_ptr(), cols)
     return out
 
 
