@@ -42,17 +42,20 @@ constexpr int kDgStageBytes = 2 * kDgTileBytes;
 // thread stores it with TMA, which writes whole lines and clips what lies outside the
 // matrix. (Stored from registers, a warp's 16-byte stores went to 32 different rows; the
 // dh product of a 4096 x 4096 x 14336 step, which reads two and writes three matrices in
-// its epilogue, took 490 us that way.) Plain products use chunks of 64 columns, those
-// with three outputs 32, double-buffered either way.
+// its epilogue, took 490 us that way.) Plain products use chunks of 64 columns and four
+// buffers (with a short reduction, as of the weights' gradients over few tokens, the stores
+// are the kernel), those with three outputs 32 columns and two.
 template <int EPI>
 struct DenseCfg {
   static constexpr int kChunk = EPI == 0 ? 64 : 32;
   static constexpr int kOuts = EPI == 0 ? 1 : 3;
-  static constexpr int kStages = EPI == 0 ? 6 : 5;
+  static constexpr int kSets = EPI == 0 ? 4 : 2;
+  static constexpr int kStages = 5;
   static constexpr int kBufBytes = 128 * kChunk * 2;
   static constexpr int kSetBytes = kOuts * kBufBytes;
   static constexpr size_t kSmem =
-      1024 + size_t(kStages) * kDgStageBytes + 2 * size_t(kSetBytes) + 256;
+      1024 + size_t(kStages) * kDgStageBytes + kSets * size_t(kSetBytes) + 256;
+  static_assert(kSmem <= 227 * 1024, "one block's shared memory");
 };
 
 struct DenseProblem {
@@ -230,7 +233,7 @@ __global__ void __launch_bounds__(kDgThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* staging = smem + size_t(kS) * kDgStageBytes;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(staging + 2 * Cfg::kSetBytes);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(staging + Cfg::kSets * Cfg::kSetBytes);
   uint64_t* full_bar = bars;
   uint64_t* empty_bar = bars + kS;
   uint64_t* tfull_bar = bars + 2 * kS;
@@ -524,8 +527,8 @@ __global__ void __launch_bounds__(kDgThreads, 1)
           else
             mbar_arrive(smem_u32(&tempty_bar[acc]));
         }
-        // this set's previous stores (two chunks ago) have read it
-        if (storer) bulk_wait_read<1>();
+        // this set's previous stores (kSets chunks ago) have read it
+        if (storer) bulk_wait_read<Cfg::kSets - 1>();
         __syncwarp();
         epilogue_barrier();
 #pragma unroll
@@ -548,7 +551,7 @@ __global__ void __launch_bounds__(kDgThreads, 1)
           bulk_commit();
         }
         __syncwarp();
-        set ^= 1;
+        if (++set == Cfg::kSets) set = 0;
       }
       if (++acc == 2) {
         acc = 0;

@@ -170,7 +170,12 @@ cudaError_t launch(GemmLaunch& L, const DeviceInfo& d, cudaStream_t st) {
   if (L.P.n_problems > 1) {
     const int late = workers - L.P.first_tiles % workers;   // == workers: no remainder
     const int rest = L.P.total_tiles - L.P.first_tiles;
-    const int k0 = q0.kb[0] + q0.kb[1], k1 = L.P.p[1].kb[0] + L.P.p[1].kb[1];
+    // a tile costs its k-blocks, and at least its epilogue (about 2 us of a pair, 1 us of a
+    // single CTA)
+    const int least = PAIR ? 7 : 5;
+    int k0 = q0.kb[0] + q0.kb[1], k1 = L.P.p[1].kb[0] + L.P.p[1].kb[1];
+    if (k0 < least) k0 = least;
+    if (k1 < least) k1 = least;
     int extra = (k0 + k1 / 2) / k1;
     if (late < workers && extra > rest / late) extra = rest / late;
     if (late < workers) L.P.extra = extra;
@@ -189,13 +194,42 @@ cudaError_t launch_any(GemmLaunch& L, bool pair, const DeviceInfo& d, cudaStream
               : launch<__nv_bfloat16, EPI, false>(L, d, st);
 }
 
-// CTA pairs on 256 x 256 tiles once there are enough of them for every pair of SMs.
-bool use_pairs(int64_t m, int64_t n, int cols, const DeviceInfo& d) {
-  return ceil_div(m, 256) * ceil_div(n, cols) >= d.sms / 2;
+// How a product of `tokens` rows, `n` columns (of one of gate / up) and `kb` k-blocks runs:
+// on CTA pairs, on single CTAs, or streaming its weights with a split reduction. Estimates in
+// microseconds, from measurements on B200: a k-block of 64 takes about 0.3 us in a 256 x 256
+// tile of a pair, 0.21 in a 128 x 128 tile of one CTA (the rate at which MMAs are issued),
+// and the split reduction ends with about 3.5 us of exchange more. Up to 128 tokens the
+// weights are streamed in any case.
+enum Shape { kPairs, kSingle, kStream };
+
+int stream_ranks(int64_t tiles, int64_t kb, int sms) {
+  int ranks = 1;
+  while (ranks < 8 && tiles * ranks * 2 <= 2 * sms && ranks * 2 <= kb) ranks *= 2;
+  return ranks;
 }
 
-// One product over at most 128 tokens: weights streamed by clusters that split the
-// reduction until there are about two CTAs an SM.
+// The weights' gradients run on CTA pairs once there are enough tiles for every pair of SMs
+// and a tile's reduction over the tokens is longer than its epilogue (d=4096, f=14336: 319 us
+// on pairs and 385 on single CTAs for 512 tokens, 209 and 192 for 128).
+bool use_pairs(int64_t f, int64_t d, int64_t tokens, const DeviceInfo& dev) {
+  return tokens > 448 && 3 * ceil_div(f, 256) * ceil_div(d, 256) >= dev.sms / 2;
+}
+
+Shape choose(int64_t tokens, int64_t n, int64_t kb, bool glu, const DeviceInfo& d) {
+  if (tokens <= moe::kStreamTokens) return kStream;
+  const int64_t cols = glu ? 2 * n : n;
+  const int64_t t256 = ceil_div(tokens, 256) * ceil_div(cols, 256);
+  const int64_t t128 = ceil_div(tokens, 128) * ceil_div(cols, 128);
+  const int ranks = stream_ranks(t128, kb, d.sms);
+  const double pairs = ceil_div(t256, d.sms / 2) * kb * 0.30;
+  const double single = ceil_div(t128, d.sms) * kb * 0.21;
+  const double stream = ceil_div(t128 * ranks, d.sms) * ceil_div(kb, ranks) * 0.21 + 3.5;
+  if (stream < pairs && stream < single) return kStream;
+  return pairs <= single ? kPairs : kSingle;
+}
+
+// One product whose weights are streamed by clusters that split the reduction until there
+// are about two CTAs an SM.
 struct StreamLaunch {
   moe::StreamMaps maps;
   moe::StreamParams P = {};
@@ -213,10 +247,9 @@ struct StreamLaunch {
 
 template <typename T, int EPI, int NB>
 cudaError_t launch_stream_columns(StreamLaunch& L, const DeviceInfo& d, cudaStream_t st) {
-  const int tiles = int(ceil_div(L.P.N, EPI == moe::kGemmGluForward ? 64 : 128));
-  const int total = L.P.kb[0] + L.P.kb[1];
-  int ranks = 1;
-  while (ranks < 8 && tiles * ranks * 2 <= 2 * d.sms && ranks * 2 <= total) ranks *= 2;
+  L.P.t_tiles = int(ceil_div(L.P.T, moe::kStreamTokens));
+  const int64_t tiles = L.P.t_tiles * ceil_div(L.P.N, EPI == moe::kGemmGluForward ? 64 : 128);
+  const int ranks = stream_ranks(tiles, L.P.kb[0] + L.P.kb[1], d.sms);
   L.P.status = d.status;
   return launch_overlapped(moe::stream_gemm_kernel<T, EPI, NB>, dim3(unsigned(tiles * ranks)),
                            dim3(moe::kStreamThreads), moe::StreamCfg<NB>::kSmem, st, ranks, L.maps,
@@ -308,62 +341,63 @@ int moe_gated_ffn_forward(int act, int dtype, int64_t T, int64_t d, int64_t f, c
   if (int s = device_info(&dev)) return s;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int m = int(T);
-  if (T <= moe::kStreamMaxTokens) {
-    StreamLaunch up_gemm;
-    up_gemm.half = dtype == MOE_DTYPE_FP16;
-    up_gemm.P.T = m;
-    up_gemm.P.N = int(f);
-    up_gemm.P.kb[0] = int(ceil_div(d, 64));
-    up_gemm.P.act = act;
-    up_gemm.P.hidden = workspace;
-    up_gemm.P.gate = gate;
-    up_gemm.P.up = up;
-    up_gemm.weights(0, W1, f, d, 64);
-    up_gemm.weights(1, W3, f, d, 64);
-    up_gemm.tokens(0, x, d, ldx);
-    cudaError_t e = launch_stream<moe::kGemmGluForward>(up_gemm, *dev, st);
-    if (e != cudaSuccess) return cuda_error(e, "gated feed-forward gate/up launch");
-    StreamLaunch down;
-    down.half = up_gemm.half;
-    down.P.T = m;
-    down.P.N = int(d);
-    down.P.kb[0] = int(ceil_div(f, 64));
-    down.P.early = 1;
-    down.P.out = out;
-    down.P.ldo = ldo;
-    down.weights(0, W2, d, f, 128);
-    down.tokens(0, workspace, f, f);
-    e = launch_stream<moe::kGemmPlain>(down, *dev, st);
-    if (e != cudaSuccess) return cuda_error(e, "gated feed-forward down launch");
-    return MOE_OK;
-  }
-  {
+  const int half = dtype == MOE_DTYPE_FP16;
+  cudaError_t e;
+  bool overlapped = false;       // the first kernel lets the second load weights early
+  const Shape first = choose(T, f, ceil_div(d, 64), true, *dev);
+  if (first == kStream) {
+    StreamLaunch L;
+    L.half = half;
+    L.P.T = m;
+    L.P.N = int(f);
+    L.P.kb[0] = int(ceil_div(d, 64));
+    L.P.act = act;
+    L.P.hidden = workspace;
+    L.P.gate = gate;
+    L.P.up = up;
+    L.weights(0, W1, f, d, 64);
+    L.weights(1, W3, f, d, 64);
+    L.tokens(0, x, d, ldx);
+    e = launch_stream<moe::kGemmGluForward>(L, *dev, st);
+    overlapped = true;
+  } else {
     GemmLaunch L;
-    L.half = dtype == MOE_DTYPE_FP16;
-    const bool pair = use_pairs(T, f, 128, *dev);
+    L.half = half;
+    const bool pair = first == kPairs;
     const int a = L.map(x, T, d, ldx, 128);
     const int b1 = L.map(W1, f, d, d, pair ? 128 : 64);
     const int b3 = L.map(W3, f, d, d, pair ? 128 : 64);
     const int o0 = L.map(workspace, T, f, f, 128, 32);
     const int o1 = gate ? L.map(gate, T, f, f, 128, 32) : o0;
     const int o2 = gate ? L.map(up, T, f, f, 128, 32) : o0;
-    if (!L.ok) return set_error(MOE_CUDA_ERROR, "tensor map encoding failed");
     L.product(m, int(f), pair ? 256 : 128, pair ? 128 : 64, d, 0, a, a, b1, b3, 0, 0, o0, o1, o2);
     L.P.save = gate != nullptr;
     L.P.act = act;
-    const cudaError_t e = launch_any<moe::kGemmGluForward>(L, pair, *dev, st);
-    if (e != cudaSuccess) return cuda_error(e, "gated feed-forward gate/up launch");
+    e = launch_any<moe::kGemmGluForward>(L, pair, *dev, st);
   }
-  GemmLaunch L;
-  L.half = dtype == MOE_DTYPE_FP16;
-  const bool pair = use_pairs(T, d, 256, *dev);
-  const int a = L.map(workspace, T, f, f, 128);
-  const int b = L.map(W2, d, f, f, 128);
-  const int o = L.map(out, T, d, ldo, 128);
-  if (!L.ok) return set_error(MOE_CUDA_ERROR, "tensor map encoding failed");
-  const int tile = pair ? 256 : 128;
-  L.product(m, int(d), tile, tile, f, 0, a, a, b, b, 0, 0, o);
-  const cudaError_t e = launch_any<moe::kGemmPlain>(L, pair, *dev, st);
+  if (e != cudaSuccess) return cuda_error(e, "gated feed-forward gate/up launch");
+  const Shape second = choose(T, d, ceil_div(f, 64), false, *dev);
+  if (second == kStream) {
+    StreamLaunch L;
+    L.half = half;
+    L.P.T = m;
+    L.P.N = int(d);
+    L.P.kb[0] = int(ceil_div(f, 64));
+    L.P.early = overlapped;
+    L.P.out = out;
+    L.P.ldo = ldo;
+    L.weights(0, W2, d, f, 128);
+    L.tokens(0, workspace, f, f);
+    e = launch_stream<moe::kGemmPlain>(L, *dev, st);
+  } else {
+    GemmLaunch L;
+    L.half = half;
+    const bool pair = second == kPairs;
+    const int tile = pair ? 256 : 128;
+    const int a = L.map(workspace, T, f, f, 128), b = L.map(W2, d, f, f, 128);
+    L.product(m, int(d), tile, tile, f, 0, a, a, b, b, 0, 0, L.map(out, T, d, ldo, 128));
+    e = launch_any<moe::kGemmPlain>(L, pair, *dev, st);
+  }
   if (e != cudaSuccess) return cuda_error(e, "gated feed-forward down launch");
   return MOE_OK;
 }
@@ -407,64 +441,71 @@ int moe_gated_ffn_backward(int act, int dtype, int64_t T, int64_t d, int64_t f, 
   char* ws = static_cast<char*>(workspace);
   void *dgate = ws, *dup = ws + plane, *hidden = ws + 2 * plane;
   const int m = int(T);
-  const bool stream_path = T <= moe::kStreamMaxTokens;
-  if (stream_path) {
-    StreamLaunch dh;
-    dh.half = dtype == MOE_DTYPE_FP16;
-    dh.P.T = m;
-    dh.P.N = int(f);
-    dh.P.kb[0] = int(ceil_div(d, 64));
-    dh.P.a_mn = 1;
-    dh.P.act = act;
-    dh.P.gate = const_cast<void*>(gate);
-    dh.P.up = const_cast<void*>(up);
-    dh.P.dgate = dgate;
-    dh.P.dup = dup;
-    dh.P.hidden = hidden;
-    dh.weights(0, W2, d, f, 64);
-    dh.tokens(0, dout, d, lddout);
-    cudaError_t e = launch_stream<moe::kGemmGluBackward>(dh, *dev, st);
-    if (e != cudaSuccess) return cuda_error(e, "gated feed-forward dh launch");
-    if (dx) {
-      StreamLaunch gx;
-      gx.half = dh.half;
-      gx.P.T = m;
-      gx.P.N = int(d);
-      gx.P.kb[0] = gx.P.kb[1] = int(ceil_div(f, 64));
-      gx.P.a_mn = 1;
-      gx.P.early = 1;
-      gx.P.out = dx;
-      gx.P.ldo = lddx;
-      gx.weights(0, W1, f, d, 64);
-      gx.weights(1, W3, f, d, 64);
-      gx.tokens(0, dgate, f, f);
-      gx.tokens(1, dup, f, f);
-      e = launch_stream<moe::kGemmPlain>(gx, *dev, st);
-      if (e != cudaSuccess) return cuda_error(e, "gated feed-forward dx launch");
-    }
-    if (!dW1 && !dW3 && !dW2) return MOE_OK;
+  const int half = dtype == MOE_DTYPE_FP16;
+  cudaError_t e;
+  bool overlapped = false;       // the first kernel lets the second load weights early
+  const Shape first = choose(T, f, ceil_div(d, 64), false, *dev);
+  if (first == kStream) {
+    StreamLaunch L;
+    L.half = half;
+    L.P.T = m;
+    L.P.N = int(f);
+    L.P.kb[0] = int(ceil_div(d, 64));
+    L.P.a_mn = 1;
+    L.P.act = act;
+    L.P.gate = const_cast<void*>(gate);
+    L.P.up = const_cast<void*>(up);
+    L.P.dgate = dgate;
+    L.P.dup = dup;
+    L.P.hidden = hidden;
+    L.weights(0, W2, d, f, 64);
+    L.tokens(0, dout, d, lddout);
+    e = launch_stream<moe::kGemmGluBackward>(L, *dev, st);
+    overlapped = true;
   } else {
     GemmLaunch L;
-    L.half = dtype == MOE_DTYPE_FP16;
-    const bool pair = use_pairs(T, f, 256, *dev);
-    const int a = L.map(dout, T, d, lddout, 128);
-    const int b = L.map(W2, d, f, f, 64);
+    L.half = half;
+    const bool pair = first == kPairs;
+    const int tile = pair ? 256 : 128;
+    const int a = L.map(dout, T, d, lddout, 128), b = L.map(W2, d, f, f, 64);
     const int o0 = L.map(hidden, T, f, f, 128, 32), o1 = L.map(dgate, T, f, f, 128, 32);
     const int o2 = L.map(dup, T, f, f, 128, 32);
-    if (!L.ok) return set_error(MOE_CUDA_ERROR, "tensor map encoding failed");
-    const int tile = pair ? 256 : 128;
     L.product(m, int(f), tile, tile, d, 0, a, a, b, b, 0, 1, o0, o1, o2);
     L.P.gate = gate;
     L.P.up = up;
     L.P.act = act;
-    const cudaError_t e = launch_any<moe::kGemmGluBackward>(L, pair, *dev, st);
-    if (e != cudaSuccess) return cuda_error(e, "gated feed-forward dh launch");
+    e = launch_any<moe::kGemmGluBackward>(L, pair, *dev, st);
+  }
+  if (e != cudaSuccess) return cuda_error(e, "gated feed-forward dh launch");
+  const bool weights = dW1 || dW3 || dW2;
+  const Shape third = choose(T, d, 2 * ceil_div(f, 64), false, *dev);
+  // dx runs in one launch with the weights' gradients, its long tiles beside their short
+  // ones, unless there are so few tokens that reading W1 and W3 is all it does (d=4096,
+  // f=14336: 169 us streamed and 178 together for 16 tokens, 195 and 192 for 128).
+  const bool stream_dx = dx && third == kStream && (!weights || T <= 32);
+  if (stream_dx) {
+    StreamLaunch L;
+    L.half = half;
+    L.P.T = m;
+    L.P.N = int(d);
+    L.P.kb[0] = L.P.kb[1] = int(ceil_div(f, 64));
+    L.P.a_mn = 1;
+    L.P.early = overlapped;
+    L.P.out = dx;
+    L.P.ldo = lddx;
+    L.weights(0, W1, f, d, 64);
+    L.weights(1, W3, f, d, 64);
+    L.tokens(0, dgate, f, f);
+    L.tokens(1, dup, f, f);
+    e = launch_stream<moe::kGemmPlain>(L, *dev, st);
+    if (e != cudaSuccess) return cuda_error(e, "gated feed-forward dx launch");
+    if (!weights) return MOE_OK;
   }
   GemmLaunch L;
-  L.half = dtype == MOE_DTYPE_FP16;
-  const bool pair = use_pairs(f, d, 256, *dev);
+  L.half = half;
+  const bool pair = weights ? use_pairs(f, d, T, *dev) : third == kPairs;
   const int tile = pair ? 256 : 128;
-  if (dx && !stream_path) {
+  if (dx && !stream_dx) {
     const int a0 = L.map(dgate, T, f, f, 128), a1 = L.map(dup, T, f, f, 128);
     const int b0 = L.map(W1, f, d, d, 64), b1 = L.map(W3, f, d, d, 64);
     L.product(m, int(d), tile, tile, f, f, a0, a1, b0, b1, 0, 1, L.map(dx, T, d, lddx, 128));
@@ -485,7 +526,7 @@ int moe_gated_ffn_backward(int act, int dtype, int64_t T, int64_t d, int64_t f, 
     L.product(int(d), int(f), tile, tile, T, 0, a, a, b, b, 1, 1, L.map(dW2, d, f, f, 128));
   }
   if (!L.ok) return set_error(MOE_CUDA_ERROR, "tensor map encoding failed");
-  const cudaError_t e = launch_any<moe::kGemmPlain>(L, pair, *dev, st);
+  e = launch_any<moe::kGemmPlain>(L, pair, *dev, st);
   if (e != cudaSuccess) return cuda_error(e, "gated feed-forward gradient launch");
   return MOE_OK;
 }

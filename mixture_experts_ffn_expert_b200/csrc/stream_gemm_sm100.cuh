@@ -1,9 +1,11 @@
-// stream_gemm_sm100.cuh - products of the gated feed-forward block for up to 128 tokens,
-// where the time is that of reading the weights once.
+// stream_gemm_sm100.cuh - products of the gated feed-forward block for few tokens, where the
+// time is that of reading the weights, and for more tokens where the other kernels' tiles
+// would leave SMs idle (a long reduction over few tiles).
 //
 // The weights are the 128-row operand of tcgen05.mma and the tokens its N columns (16, 32,
-// 64 or 128, padded with zeros by TMA), so a weight tile is read by one CTA only and the
-// tensor work does not grow with a padded token tile. The reduction is split over the CTAs
+// 64 or 128, padded with zeros by TMA; more than 128 tokens are tiled by 128), so up to 128
+// tokens a weight tile is read once and the tensor work does not grow with a padded token
+// tile. The reduction is split over the CTAs
 // of a cluster (1, 2, 4 or 8), as many as it takes to give every SM a stream of its own:
 // two CTAs share an SM, each with its own ring of TMA stages, which keeps about 200 KB of
 // loads in flight an SM. Every rank finishes an equal share of the tile's rows: each CTA
@@ -24,7 +26,7 @@
 namespace moe {
 
 constexpr int kStreamThreads = 224;
-constexpr int kStreamMaxTokens = 128;
+constexpr int kStreamTokens = 128;          // a token tile
 
 template <int NB>
 struct StreamCfg {
@@ -43,6 +45,7 @@ struct StreamCfg {
 
 struct StreamParams {
   int T, N;                 // tokens; rows of the weights (columns of the output)
+  int t_tiles;              // token tiles
   int kb[2];                // k-blocks of 64 in the two segments of the reduction
   int a_mn;                 // weights read along their columns
   int early;                // weights may be loaded before the predecessor has finished
@@ -91,8 +94,11 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
   const int lane = threadIdx.x & 31;
   const int ranks = static_cast<int>(cluster_nctarank());
   const int rank = static_cast<int>(cluster_ctarank());
+  // clusters that share a weight tile are neighbours
   const int tile = blockIdx.x / ranks;
-  const int row0 = tile * kRows;
+  const int row0 = tile / P.t_tiles * kRows;
+  const int token0 = tile % P.t_tiles * kStreamTokens;
+  const int tokens = min(P.T - token0, kStreamTokens);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kS; ++s) {
@@ -147,7 +153,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
           }
         } else {
           mbar_arrive_expect_tx(fb, NB * 128);
-          tma_load_2d(dst + kDgTileBytes, &maps.b[seg], fb, k0, 0);
+          tma_load_2d(dst + kDgTileBytes, &maps.b[seg], fb, k0, token0);
         }
         issued_mask |= 1u << s;
         issued_par = (issued_par & ~(1u << s)) | (ph << s);
@@ -227,16 +233,16 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
       // token by token, so that a warp's store is one run of consecutive words for every
       // owner (16-byte stores of four tokens a lane, a row apart, took twice as long)
       const uint32_t dst =
-          mapa_shared(smem_u32(red), owner) + (rank * P.T * rows_each + local) * 4;
+          mapa_shared(smem_u32(red), owner) + (rank * tokens * rows_each + local) * 4;
 #pragma unroll 1
-      for (int c = 0; c < P.T; c += 16) {
+      for (int c = 0; c < tokens; c += 16) {
         uint32_t v[16];
         tmem_ld_8cols(lane_base + c, *reinterpret_cast<uint32_t(*)[8]>(v));
         tmem_ld_8cols(lane_base + c + 8, *reinterpret_cast<uint32_t(*)[8]>(v + 8));
         tmem_ld_wait();
 #pragma unroll
         for (int j = 0; j < 16; ++j)
-          if (c + j < P.T) st_cluster_f32(dst + (c + j) * rows_each * 4, v[j]);
+          if (c + j < tokens) st_cluster_f32(dst + (c + j) * rows_each * 4, v[j]);
       }
     }
     tc_fence_before_sync();
@@ -246,7 +252,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
   // ------------------------------------------------------------ reduction and epilogue
   // This rank's share of the tile's output columns, four at a time.
   const int quads = share / 4;
-  for (int i = threadIdx.x; i < P.T * quads; i += kStreamThreads) {
+  for (int i = threadIdx.x; i < tokens * quads; i += kStreamThreads) {
     const int t = i / quads;
     const int local = (i - t * quads) * 4;
     const int n = row0 + rank * share + local;
@@ -256,13 +262,13 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       if (k < ranks) {
-        const float4 p = *reinterpret_cast<const float4*>(part + k * P.T * rows_each);
+        const float4 p = *reinterpret_cast<const float4*>(part + k * tokens * rows_each);
         v[0] += p.x;
         v[1] += p.y;
         v[2] += p.z;
         v[3] += p.w;
         if (EPI == kGemmGluForward) {
-          const float4 w = *reinterpret_cast<const float4*>(part + k * P.T * rows_each + share);
+          const float4 w = *reinterpret_cast<const float4*>(part + k * tokens * rows_each + share);
           u[0] += w.x;
           u[1] += w.y;
           u[2] += w.z;
@@ -271,10 +277,10 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
       }
     }
     if (EPI == kGemmPlain) {
-      *reinterpret_cast<uint2*>(static_cast<T*>(P.out) + t * P.ldo + n) =
+      *reinterpret_cast<uint2*>(static_cast<T*>(P.out) + (token0 + t) * P.ldo + n) =
           make_uint2(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]));
     } else if (EPI == kGemmGluForward) {
-      const long long at = static_cast<long long>(t) * P.N + n;
+      const long long at = static_cast<long long>(token0 + t) * P.N + n;
       float h[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) h[j] = act_value(v[j], P.act) * u[j];
@@ -287,7 +293,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
             make_uint2(pack2<T>(u[0], u[1]), pack2<T>(u[2], u[3]));
       }
     } else {
-      const long long at = static_cast<long long>(t) * P.N + n;
+      const long long at = static_cast<long long>(token0 + t) * P.N + n;
       const uint2 g2 = *reinterpret_cast<const uint2*>(static_cast<const T*>(P.gate) + at);
       const uint2 u2 = *reinterpret_cast<const uint2*>(static_cast<const T*>(P.up) + at);
       const float2 ga = unpack2<T>(g2.x), gb = unpack2<T>(g2.y);
