@@ -69,7 +69,7 @@ struct DenseProblem {
 
 struct DenseParams {
   DenseProblem p[kDgMaxProblems];
-  int n_problems, total_tiles;
+  int n_problems, total_tiles, n_maps;
   int first_tiles;                  // tiles of problem 0 (the costly ones)
   int extra;                        // see tile_of
   const void *gate, *up;            // dh: the saved pre-activations (M, N)
@@ -265,6 +265,8 @@ __global__ void __launch_bounds__(kDgThreads, 1)
     *s_abort = 0;
     fence_mbar_init();
   }
+  // the descriptors' first use would otherwise wait for them after the predecessor's end
+  if (warp == 6 && lane < P.n_maps) tma_prefetch_desc(&maps.m[lane]);
   if (warp == 1) {
     if (PAIR) {
       tmem_alloc_pair(smem_u32(s_tmem), kTmem);

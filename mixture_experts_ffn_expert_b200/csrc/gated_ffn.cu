@@ -181,6 +181,7 @@ cudaError_t launch(GemmLaunch& L, const DeviceInfo& d, cudaStream_t st) {
     if (late < workers) L.P.extra = extra;
   }
   L.P.status = d.status;
+  L.P.n_maps = L.n_maps;
   return launch_overlapped(moe::dense_gemm_kernel<T, EPI, PAIR>,
                            dim3(PAIR ? 2 * workers : workers), dim3(moe::kDgThreads),
                            moe::DenseCfg<EPI>::kSmem, st, PAIR ? 2 : 1, L.maps, L.P);

@@ -110,6 +110,8 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
     fence_mbar_init();
     tma_prefetch_desc(&maps.a[0]);
     tma_prefetch_desc(&maps.b[0]);
+    if (EPI == kGemmGluForward || P.kb[1] > 0) tma_prefetch_desc(&maps.a[1]);
+    if (P.kb[1] > 0) tma_prefetch_desc(&maps.b[1]);
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(s_tmem), Cfg::kTmem);
