@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(1024) norm_backward_kernel(const NormParams P,
   }
 }
 
-// Backward for rows too long for registers: dx (three reads of the row)...
+// Backward for rows too long for a block's registers: dx (the row is read twice)...
 template <typename T>
 __global__ void __launch_bounds__(1024) norm_backward_long_kernel(const NormParams P) {
   __shared__ float s_sum[2][32];

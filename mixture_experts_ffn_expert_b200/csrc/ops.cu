@@ -57,18 +57,29 @@ cudaError_t launch_norm_forward(const moe::NormParams& P, int group, cudaStream_
                            dim3(group * per_block), 0, st, 1, P, group);
 }
 
-// Tile kernels: enough rows that every SM has several (600 x 7168 bf16 forward: 8.0 us, 9.6
-// with a block a row).
-constexpr int64_t kTileMinRows = 592;
+// Rows from which the tile kernels run. In general when every SM has four; with two for
+// rows of 4097 to 8192 (forward, 300 x 7168 bf16: 6.3 us, 7.8 with a block a row) and for
+// unaligned rows above 4096 (300 x 7001 bf16: 10.1 and 14.9).
+int64_t tile_rows_forward(int cols, bool vec) {
+  return cols > 4096 && (cols <= 8192 || !vec) ? 296 : 592;
+}
+// Backward: with two also from 256 to 1024 vectors a row (300 x 2048 bf16: 11.8 us, 13.7 with
+// a block a row), and always for unaligned rows of 4097 to 8192 (1 x 7001 bf16: 9.6 us; a
+// block a row would hold so many elements a thread that they spill, 20.6).
+int64_t tile_rows_backward(int cols, bool vec, int vectors) {
+  if (vec) return vectors >= 256 && vectors <= 1024 ? 296 : 592;
+  return cols > 4096 && cols <= 8192 ? 1 : 592;
+}
 constexpr size_t kTileSmem = 208 * 1024;
 // 16 column warps beside the 8 row warps (with 8, 4096 x 7168 bf16 forward took 36 us
 // instead of 26 and the backward pass up to 30% longer).
 constexpr int kColumnWarps = 16;
 
 // Rows a tile and slots, for `planes` matrices (x, and dy in the backward pass): three
-// tiles of as many rows as fit, more tiles when they are small.
+// tiles of as many rows as fit, more tiles when they are small; no more rows a tile than a
+// block has, so that with few rows several row warps share one.
 bool tile_shape(moe::NormTile* L, const moe::NormParams& P, int vec, int vpt, int column_warps,
-                size_t esize, int planes, bool contiguous, size_t* smem) {
+                size_t esize, int planes, bool contiguous, int sms, size_t* smem) {
   const int n = P.cols / vec;
   L->group = round32((n + vpt - 1) / vpt);
   if (L->group > column_warps * 32) return false;
@@ -78,6 +89,7 @@ bool tile_shape(moe::NormTile* L, const moe::NormParams& P, int vec, int vpt, in
   const size_t room = kTileSmem - L->weight_bytes;
   const size_t extra = vec == 1 ? 32 : 0;         // a run of bytes widened to 16-byte boundaries
   for (int rows = moe::kRowWarps; rows >= 1; rows /= 2) {
+    if (rows > 1 && int64_t(rows) * sms > P.rows + sms - 1) continue;
     const size_t slot = (size_t(P.cols) * esize * rows + extra + 127) / 128 * 128;
     const size_t tile = slot * planes;
     if (tile * 3 > room && !(rows == 1 && tile * 2 <= room)) continue;
@@ -110,8 +122,9 @@ cudaError_t launch_norm_forward_tile(const moe::NormParams& P, const moe::NormTi
   const auto kernel = moe::norm_forward_tile_kernel<T, VEC, VPT, kColumnWarps, RMS>;
   const cudaError_t e = tile_attribute(kernel, &done, d.index);
   if (e != cudaSuccess) return e;
-  return launch_overlapped(kernel, dim3(d.sms), dim3(moe::tile_threads(kColumnWarps)), smem, st, 1, P, L,
-                           d.status);
+  const int64_t blocks = P.rows < d.sms ? P.rows : d.sms;
+  return launch_overlapped(kernel, dim3(unsigned(blocks)),
+                           dim3(moe::tile_threads(kColumnWarps)), smem, st, 1, P, L, d.status);
 }
 
 // Runs the tile kernel with the fewest vectors a column thread that cover the columns; false
@@ -121,7 +134,7 @@ bool norm_forward_tile(const moe::NormParams& P, bool contiguous, const moe::Ops
                        cudaStream_t st, cudaError_t* e) {
   moe::NormTile L;
   size_t smem;
-  if (tile_shape(&L, P, VEC, VPT, kColumnWarps, sizeof(T), 1, contiguous, &smem)) {
+  if (tile_shape(&L, P, VEC, VPT, kColumnWarps, sizeof(T), 1, contiguous, d.sms, &smem)) {
     *e = launch_norm_forward_tile<T, VEC, VPT, RMS>(P, L, smem, d, st);
     return true;
   }
@@ -135,7 +148,7 @@ cudaError_t norm_forward_any(const moe::NormParams& P, bool vec, bool contiguous
   constexpr int V = 16 / sizeof(T);
   // Few rows: as many threads a row as it has vectors (latency). Many unaligned rows that
   // are not contiguous: short ones a warp each, no block barrier in the statistics.
-  const bool few = P.rows < kTileMinRows;
+  const bool few = P.rows < tile_rows_forward(P.cols, vec);
   if (!few && (vec || contiguous)) {
     cudaError_t e;
     if (vec ? (P.rms ? norm_forward_tile<T, V, true, 1, 4>(P, contiguous, d, st, &e)
@@ -185,7 +198,9 @@ cudaError_t launch_norm_backward_tile(const moe::NormParams& P, const moe::NormT
   const auto kernel = moe::norm_backward_tile_kernel<T, VEC, VPT, kColumnWarps, RMS, GRADW>;
   const cudaError_t e = tile_attribute(kernel, &done, d.index);
   if (e != cudaSuccess) return e;
+  // no more blocks than partial rows in the workspace: min(rows, kNormBlocks)
   *blocks = d.sms < kNormBlocks ? d.sms : kNormBlocks;
+  if (P.rows < *blocks) *blocks = static_cast<int>(P.rows);
   return launch_overlapped(kernel, dim3(*blocks), dim3(moe::tile_threads(kColumnWarps)), smem, st, 1, P, L,
                            d.status);
 }
@@ -195,7 +210,7 @@ bool norm_backward_tile(const moe::NormParams& P, bool contiguous, const moe::Op
                         int* blocks, cudaStream_t st, cudaError_t* e) {
   moe::NormTile L;
   size_t smem;
-  if (tile_shape(&L, P, VEC, VPT, kColumnWarps, sizeof(T), 2, contiguous, &smem)) {
+  if (tile_shape(&L, P, VEC, VPT, kColumnWarps, sizeof(T), 2, contiguous, d.sms, &smem)) {
     // the groups' sums meet in the ring: two planes of fp32 columns
     const bool meet = kColumnWarps * 32 / L.group > 1;
     if (meet && smem - L.weight_bytes < size_t(P.cols) * 8) return false;
@@ -211,7 +226,7 @@ template <typename T, bool RMS, bool GRADW>
 cudaError_t norm_backward_any(const moe::NormParams& P, bool vec, bool contiguous,
                               const moe::OpsDevice& d, int* blocks, cudaStream_t st) {
   constexpr int V = 16 / sizeof(T);
-  if (P.rows >= kTileMinRows && (vec || contiguous)) {
+  if (P.rows >= tile_rows_backward(P.cols, vec, P.cols / V) && (vec || contiguous)) {
     cudaError_t e;
     if (vec ? norm_backward_tile<T, V, RMS, GRADW, 1, 4>(P, contiguous, d, blocks, st, &e)
             : norm_backward_tile<T, 1, RMS, GRADW, 4, 32>(P, contiguous, d, blocks, st, &e))
@@ -220,17 +235,11 @@ cudaError_t norm_backward_any(const moe::NormParams& P, bool vec, bool contiguou
   if (vec) {
     const int n = P.cols / V;
     if (n <= 1024) return launch_norm_backward<T, V, 1, RMS, GRADW>(P, round32(n), blocks, st);
-    if (n <= 2048)
-      return launch_norm_backward<T, V, 2, RMS, GRADW>(P, round32((n + 1) / 2), blocks, st);
-    if (n <= 4096)
-      return launch_norm_backward<T, V, 4, RMS, GRADW>(P, round32((n + 3) / 4), blocks, st);
-  } else {
-    if (P.cols <= 4096)
-      return launch_norm_backward<T, 1, 4, RMS, GRADW>(P, round32((P.cols + 3) / 4), blocks, st);
-    if (P.cols <= 16384)
-      return launch_norm_backward<T, 1, 16, RMS, GRADW>(P, round32((P.cols + 15) / 16), blocks,
-                                                        st);
+  } else if (P.cols <= 4096) {
+    return launch_norm_backward<T, 1, 4, RMS, GRADW>(P, round32((P.cols + 3) / 4), blocks, st);
   }
+  // Wider rows from global memory, three passes (300 x 16384 fp32: 41 us; held in the
+  // registers of a block, spilling, 90).
   cudaError_t e = cudaSuccess;
   if (GRADW) {                          // before dx, which may overwrite dy
     *blocks = static_cast<int>(P.rows < 32 ? P.rows : 32);
