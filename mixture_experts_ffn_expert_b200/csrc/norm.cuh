@@ -7,9 +7,10 @@
 //   dx = rstd * (g - mean(g) - xh * mean(g * xh)) (rms: without mean(g))
 //   dweight = sum over rows of dy * xh,   dbias = sum over rows of dy
 //
-// Both passes are bound by memory: the forward reads x and writes y, the backward reads
-// x and dy and writes dx, once each. A row is held in registers between its statistics
-// and its output. Statistics, products and sums are fp32; the variance is the mean of
+// Both passes are to be bound by memory: the forward reads x and writes y, the backward
+// reads x and dy and writes dx, once each. A row is held in registers (few rows) or shared
+// memory (many) between its statistics and its output; only rows too long for either are
+// read again. Statistics, products and sums are fp32; the variance is the mean of
 // squared differences from the mean (not a difference of two large sums). Results are
 // rounded once, on the store. No atomics: the weight's gradient is summed per thread
 // over the rows a block walks, then over the blocks in a fixed order, so equal inputs
@@ -369,12 +370,12 @@ __global__ void __launch_bounds__(256) norm_backward_long_sum_kernel(const NormP
 }
 
 // ------------------------------------------------------------------ tile kernels
-// Many rows: one persistent block an SM walks its share of the rows in tiles of 1 to 8
+// Many rows: one persistent block an SM walks its share of the rows in tiles of 1 to 32
 // rows, as a pipeline of warps over a ring of shared-memory slots:
 //   one thread brings tiles in with bulk copies (cp.async.bulk), as far ahead as there are
 //     slots, so that the loads in flight depend neither on registers nor on occupancy;
-//   8 row warps sum what a row needs along it (8 / rows warps a row; a lane holds many
-//     elements, so shuffles are few);
+//   8 row warps sum what a row needs along it (8 / rows warps a row, or rows / 8 rows a
+//     warp; a lane holds many elements, so shuffles are few);
 //   the column warps merge those sums, keep their columns' weights, and in the backward
 //     pass their gradients, in registers over all rows, and write the output.
 // Barriers of the ring order them tile by tile (full, summed, free); there is no block-wide
@@ -387,10 +388,11 @@ __global__ void __launch_bounds__(256) norm_backward_long_sum_kernel(const NormP
 // before it, and its elements are read one by one.
 constexpr int kRowWarps = 8;
 constexpr int kTileMaxSlots = 8;
+constexpr int kTileMaxRows = 32;
 constexpr int tile_threads(int column_warps) { return (kRowWarps + column_warps + 1) * 32; }
 
 struct NormTile {
-  int rows;                // a tile: 1, 2, 4 or 8
+  int rows;                // a tile: 1, 2, 4, 8, 16 or 32
   int slots;
   int group;               // column threads that cover the columns once
   int contiguous;          // rows follow one another: one copy a tile
@@ -400,7 +402,7 @@ struct NormTile {
 
 struct TileShared {
   uint64_t full[kTileMaxSlots], summed[kTileMaxSlots], free[kTileMaxSlots];
-  float2 part[kTileMaxSlots][kRowWarps];
+  float2 part[kTileMaxSlots][kTileMaxRows];
   int abort;
 };
 
@@ -630,7 +632,7 @@ __global__ void __launch_bounds__(tile_threads(CW), 1)
   const int tiles = static_cast<int>((hi - lo + L.rows - 1) / L.rows);
   const uint32_t row_bytes = static_cast<uint32_t>(P.cols) * sizeof(T);
   const int n_vec = P.cols / VEC;
-  const int wpr = kRowWarps / L.rows;
+  const int wpr = L.rows < kRowWarps ? kRowWarps / L.rows : 1;
   int s = 0;
   uint32_t ph = 0;
   if (warp == kRowWarps + CW) {
@@ -641,7 +643,7 @@ __global__ void __launch_bounds__(tile_threads(CW), 1)
     const int my_row = warp / wpr, q = warp - my_row * wpr;
     const float own_n = static_cast<float>(part_vectors(n_vec, wpr, q) * VEC);
     const float own_inv = own_n > 0.0f ? 1.0f / own_n : 0.0f;
-    const uint32_t base = smem_u32(ring) + my_row * row_bytes + (q * 32 + lane) * kVecBytes;
+    const uint32_t base = smem_u32(ring) + (q * 32 + lane) * kVecBytes;
     const uint32_t step = wpr * 32 * kVecBytes;
     // every lane reads the same number of vectors, the last perhaps beyond the row: masked
     const int rounds = (n_vec + wpr * 32 - 1) / (wpr * 32);
@@ -649,8 +651,8 @@ __global__ void __launch_bounds__(tile_threads(CW), 1)
     for (int t = 0; t < tiles; ++t) {
       const long long row0 = lo + static_cast<long long>(t) * L.rows;
       tile_wait(&sh.full[s], ph, &sh.abort, status);
-      if (row0 + my_row < hi) {
-        const uint32_t x = base + s * L.slot_bytes + tile_shift<T, VEC>(P, row0);
+      for (int r = my_row; r < L.rows && row0 + r < hi; r += kRowWarps) {
+        const uint32_t x = base + s * L.slot_bytes + tile_shift<T, VEC>(P, row0) + r * row_bytes;
         float sum = 0.0f, part_mean = 0.0f;
         if (!RMS) {
           f32x2 acc[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
@@ -684,7 +686,7 @@ __global__ void __launch_bounds__(tile_threads(CW), 1)
         const f32x2 both = add2(acc[0], acc[1]);
         float sq = both.x + both.y;
         sq = warp_sum(sq);
-        if (lane == 0) sh.part[s][warp] = make_float2(sum, sq);
+        if (lane == 0) sh.part[s][r * wpr + q] = make_float2(sum, sq);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sh.summed[s]));
@@ -708,7 +710,8 @@ __global__ void __launch_bounds__(tile_threads(CW), 1)
       }
     }
     const float n = static_cast<float>(P.cols), inv_n = 1.0f / n;
-    const int l = lane & 7;           // lane l (mod 8) merges what row warp l summed
+    const int parts = L.rows < kRowWarps ? kRowWarps : L.rows;
+    const int l = lane & (parts - 1);        // lane l merges the tile's l-th sum
     const float part_n = static_cast<float>(part_vectors(n_vec, wpr, l % wpr) * VEC);
     const float part_inv = part_n > 0.0f ? 1.0f / part_n : 0.0f;
     for (int t = 0; t < tiles; ++t) {
@@ -728,7 +731,7 @@ __global__ void __launch_bounds__(tile_threads(CW), 1)
       }
       for (int o = 1; o < wpr; o <<= 1) m2 += __shfl_xor_sync(0xffffffffu, m2, o);
       const float rstd = inv_sqrt(fmaf(m2, inv_n, P.eps));
-      if (warp == kRowWarps && lane < 8 && l % wpr == 0 && l / wpr < valid) {
+      if (warp == kRowWarps && lane < parts && l % wpr == 0 && l / wpr < valid) {
         if (!RMS && P.mean) P.mean[row0 + l / wpr] = mean;
         if (P.rstd) P.rstd[row0 + l / wpr] = rstd;
       }
@@ -796,7 +799,7 @@ __global__ void __launch_bounds__(tile_threads(CW), 1)
   }
   const uint32_t row_bytes = static_cast<uint32_t>(P.cols) * sizeof(T);
   const int n_vec = P.cols / VEC;
-  const int wpr = kRowWarps / L.rows;
+  const int wpr = L.rows < kRowWarps ? kRowWarps / L.rows : 1;
   int s = 0;
   uint32_t ph = 0;
   if (warp == kRowWarps + CW) {
@@ -806,26 +809,30 @@ __global__ void __launch_bounds__(tile_threads(CW), 1)
   if (warp < kRowWarps) {
     // ---- row warps: their part of the sums of g * (x - mean) and of g
     const int my_row = warp / wpr, q = warp - my_row * wpr;
-    float next_mean = 0.0f, next_rstd = 0.0f;      // loaded one tile ahead
-    if (lo + my_row < hi) {
-      if (!RMS) next_mean = P.mean[lo + my_row];
-      next_rstd = P.rstd[lo + my_row];
-    }
-    const uint32_t base = smem_u32(ring) + my_row * row_bytes + (q * 32 + lane) * kVecBytes;
+    // lane l holds the statistics of row l of the tile, loaded one tile ahead
+    float next_mean = 0.0f, next_rstd = 0.0f;
+    auto load_stats = [&](long long row) {
+      if (lane < L.rows && row + lane < hi) {
+        if (!RMS) next_mean = P.mean[row + lane];
+        next_rstd = P.rstd[row + lane];
+      }
+    };
+    load_stats(lo);
+    const uint32_t base = smem_u32(ring) + (q * 32 + lane) * kVecBytes;
     const uint32_t step = wpr * 32 * kVecBytes;
     const uint32_t w_base = smem_u32(ws) + (q * 32 + lane) * (VEC * 4);
     const int rounds = (n_vec + wpr * 32 - 1) / (wpr * 32);
     const bool last = (rounds - 1) * wpr * 32 + q * 32 + lane < n_vec;
     for (int t = 0; t < tiles; ++t) {
       const long long row0 = lo + static_cast<long long>(t) * L.rows;
-      const float mean = next_mean, rstd = next_rstd;
-      if (row0 + L.rows + my_row < hi) {
-        if (!RMS) next_mean = P.mean[row0 + L.rows + my_row];
-        next_rstd = P.rstd[row0 + L.rows + my_row];
-      }
+      const float means = next_mean, rstds = next_rstd;
+      load_stats(row0 + L.rows);
       tile_wait(&sh.full[s], ph, &sh.abort, status);
-      if (row0 + my_row < hi) {
-        const uint32_t x = base + s * 2 * L.slot_bytes + tile_shift<T, VEC>(P, row0);
+      for (int r = my_row; r < L.rows && row0 + r < hi; r += kRowWarps) {
+        const float mean = RMS ? 0.0f : __shfl_sync(0xffffffffu, means, r);
+        const float rstd = __shfl_sync(0xffffffffu, rstds, r);
+        const uint32_t x =
+            base + s * 2 * L.slot_bytes + tile_shift<T, VEC>(P, row0) + r * row_bytes;
         const f32x2 shift = make2(-mean, -mean);
         f32x2 s1[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}}, s2[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
         auto add = [&](int k) {
@@ -854,7 +861,7 @@ __global__ void __launch_bounds__(tile_threads(CW), 1)
         float c1 = b1.x + b1.y, c2 = b2.x + b2.y;
         c2 = warp_sum(c2) * rstd;
         if (!RMS) c1 = warp_sum(c1);
-        if (lane == 0) sh.part[s][warp] = make_float2(c1, c2);
+        if (lane == 0) sh.part[s][r * wpr + q] = make_float2(c1, c2);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sh.summed[s]));
@@ -892,7 +899,8 @@ __global__ void __launch_bounds__(tile_threads(CW), 1)
     }
   }
   const float inv = 1.0f / static_cast<float>(P.cols);
-  const int l = lane & 7;
+  const int parts = L.rows < kRowWarps ? kRowWarps : L.rows;
+  const int l = lane & (parts - 1);
   // lane l holds the statistics of row l of the tile, loaded one tile ahead
   float next_mean = 0.0f, next_rstd = 0.0f;
   auto load_stats = [&](long long row) {

@@ -87,7 +87,7 @@ def norm_bounds(x, w, b, dy, dtype, wdtype, kind, eps):
 SHAPES = [(1, 1), (3, 7), (1, 7168), (5, 32), (33, 33), (600, 128), (601, 129), (37, 1003),
           (700, 250), (64, 2048), (593, 2048), (9, 4100), (21, 7168), (7, 8200), (5, 16384),
           (3, 16385), (4, 33000), (2, 70000), (1777, 96), (1300, 512), (1185, 1032),
-          (1200, 2056), (1190, 7168), (1184, 8200), (1500, 4096), (1184, 16384)]
+          (5000, 64), (3001, 257), (4747, 33), (2600, 1024), (1200, 2056), (1190, 7168), (1184, 8200), (1500, 4096), (1184, 16384)]
 
 
 @pytest.mark.parametrize("kind", ["layer", "rms"])
