@@ -652,3 +652,87 @@ def test_training_step_in_a_graph_and_on_other_streams():
     assert all(torch.equal(a, b) for a, b in zip(want, ref))
     load_library()
     ops.device_status()
+
+
+FIRST_CALL = """
+import torch
+from mixture_experts_ffn_expert_b200 import ops
+g = lambda *s: torch.randn(*s, device="cuda").bfloat16()
+x, W1, W3, W2 = g(40, 64), g(72, 64), g(72, 64), g(64, 72)
+rng = torch.tensor([1, 2], device="cuda")
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    h = ops.norm_forward(x, kind="rms")
+    y, gate, up = ops.gated_ffn_forward(h, W1, W3, W2, save=True)
+    grads = ops.gated_ffn_backward(y, h, W1, W3, W2, gate, up)
+    out = ops.dropout_add_forward(y, x, 0.1, rng)
+graph.replay()
+torch.cuda.synchronize()
+assert torch.equal(out, ops.dropout_add_forward(
+    ops.gated_ffn_forward(ops.norm_forward(x, kind="rms"), W1, W3, W2), x, 0.1, rng))
+ops.device_status()
+print("captured")
+"""
+
+
+def test_first_call_of_a_process_may_be_captured():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=root, capture_output=True,
+                       text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
+
+
+def test_many_host_threads_and_streams():
+    # eight host threads, each on its own stream with its own inputs, at the same time
+    import threading
+    cases = [ffn_case(T, 136, 264, "bf16", 20 + i)
+             for i, T in enumerate((1, 7, 33, 64, 129, 200, 300, 500))]
+
+    def step(c):
+        x, W1, W3, W2, dout = c
+        h, mean, rstd = ops.norm_forward(x, save=True)
+        y, gate, up = ops.gated_ffn_forward(h, W1, W3, W2, save=True)
+        grads = ops.gated_ffn_backward(dout, h, W1, W3, W2, gate, up)
+        return (y, *grads, ops.norm_backward(grads[0], x, None, mean, rstd)[0])
+
+    want = [step(c) for c in cases]
+    torch.cuda.synchronize()
+    got, errors = [None] * len(cases), []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(10):
+                    got[i] = step(cases[i])
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:     # reported by the test's thread
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(cases))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert all(torch.equal(u, v) for u, v in zip(a, b))
+
+
+def test_same_tensor_twice():
+    # one tensor as several arguments: W1 as W3, x as residual and as the gradient
+    x, W1, _, W2, _ = ffn_case(50, 136, 264, "bf16", 30)
+    out, gate, up = ops.gated_ffn_forward(x, W1, W1, W2, save=True)
+    assert torch.equal(gate, up)
+    dx, d1, d3, d2 = ops.gated_ffn_backward(x, x, W1, W1, W2, gate, up)
+    want = ffn_bounds(*(f64(t) for t in (x, W1, W1, W2, x)), "silu", torch.bfloat16)
+    for name, got in zip(("out", "dx", "dW1", "dW3", "dW2"), (out, dx, d1, d3, d2)):
+        close(got, *want[name], name)
+    rng = torch.tensor([3, 4], device="cuda")
+    got = ops.dropout_add_forward(x, x, 0.25, rng)
+    want = O.dropout_add(f64(x), f64(x), 0.25, 3, 4)
+    close(got, want, drop_tol(f64(x), f64(x), 0.25, torch.bfloat16, want), "x twice")
