@@ -375,9 +375,11 @@ __global__ void __launch_bounds__(256) norm_backward_long_sum_kernel(const NormP
 //   one thread brings tiles in with bulk copies (cp.async.bulk), as far ahead as there are
 //     slots, so that the loads in flight depend neither on registers nor on occupancy;
 //   8 row warps sum what a row needs along it (8 / rows warps a row, or rows / 8 rows a
-//     warp; a lane holds many elements, so shuffles are few);
-//   the column warps merge those sums, keep their columns' weights, and in the backward
-//     pass their gradients, in registers over all rows, and write the output.
+//     warp; a lane holds many elements, so shuffles are few) and leave the row's finished
+//     statistics in shared memory;
+//   the column warps keep their columns' weights, and in the backward pass their
+//     gradients, in registers over all rows, and write the output. They are the longer
+//     stage and all work on one tile, so nothing that could be done before is left to them.
 // Barriers of the ring order them tile by tile (full, summed, free); there is no block-wide
 // barrier, so no part waits for another's latency. (With the row spread over a block and
 // two block reductions a row, 8192 x 2048 bf16 took 36 us forward; with tiles worked first
@@ -402,9 +404,16 @@ struct NormTile {
 
 struct TileShared {
   uint64_t full[kTileMaxSlots], summed[kTileMaxSlots], free[kTileMaxSlots];
-  float2 part[kTileMaxSlots][kTileMaxRows];
+  // a row's finished values: mean and rstd; backward: and the means of g and of g * xh
+  float4 stat[kTileMaxSlots][kTileMaxRows];
+  float2 part[2][kRowWarps];          // what several row warps sum of one row; alternate tiles
   int abort;
 };
+
+// Row warps that share rows meet here between their sums and the rows' statistics.
+__device__ __forceinline__ void row_warps_meet() {
+  asm volatile("bar.sync 3, %0;" ::"n"(kRowWarps * 32) : "memory");
+}
 
 // Wait for a phase of a ring barrier, suspended in the hardware for up to 0.1 ms a try (25
 // warps that poll would take the issue slots of those that work). A wait that gives up
@@ -607,7 +616,7 @@ __device__ __forceinline__ void tile_init(const NormTile& L, TileShared& sh, int
   if (threadIdx.x == 0) {
     for (int s = 0; s < L.slots; ++s) {
       mbar_init(smem_u32(&sh.full[s]), 1);
-      mbar_init(smem_u32(&sh.summed[s]), kRowWarps);
+      mbar_init(smem_u32(&sh.summed[s]), L.rows < kRowWarps ? L.rows : kRowWarps);
       mbar_init(smem_u32(&sh.free[s]), column_warps);
     }
     sh.abort = 0;
@@ -639,10 +648,23 @@ __global__ void __launch_bounds__(tile_threads(CW), 1)
     if (lane == 0) tile_producer<T, VEC, 1>(P, L, ring, sh, lo, hi, tiles, status);
   } else if (warp < kRowWarps) {
     // ---- row warps: the sum of this warp's part of its row, and the squared differences
-    // from the part's own mean (sum (x - m)^2 = sum (x - m_w)^2 + n_w (m_w - m)^2 later)
+    // from the part's own mean
     const int my_row = warp / wpr, q = warp - my_row * wpr;
+    const float n = static_cast<float>(P.cols), inv_n = 1.0f / n;
     const float own_n = static_cast<float>(part_vectors(n_vec, wpr, q) * VEC);
     const float own_inv = own_n > 0.0f ? 1.0f / own_n : 0.0f;
+    // the elements that the warp lane / q' of this row sums (lane < wpr)
+    const float lane_n =
+        lane < wpr ? static_cast<float>(part_vectors(n_vec, wpr, lane) * VEC) : 0.0f;
+    const float lane_inv = lane_n > 0.0f ? 1.0f / lane_n : 0.0f;
+    auto finish = [&](long long row, int r, int slot, float mean, float m2) {
+      const float rstd = inv_sqrt(fmaf(m2, inv_n, P.eps));
+      if (lane == 0) {
+        sh.stat[slot][r] = make_float4(mean, rstd, 0.0f, 0.0f);
+        if (!RMS && P.mean) P.mean[row] = mean;
+        if (P.rstd) P.rstd[row] = rstd;
+      }
+    };
     const uint32_t base = smem_u32(ring) + (q * 32 + lane) * kVecBytes;
     const uint32_t step = wpr * 32 * kVecBytes;
     // every lane reads the same number of vectors, the last perhaps beyond the row: masked
@@ -686,10 +708,24 @@ __global__ void __launch_bounds__(tile_threads(CW), 1)
         const f32x2 both = add2(acc[0], acc[1]);
         float sq = both.x + both.y;
         sq = warp_sum(sq);
-        if (lane == 0) sh.part[s][r * wpr + q] = make_float2(sum, sq);
+        if (wpr == 1) {
+          finish(row0 + r, r, s, part_mean, sq);
+        } else if (lane == 0) {
+          sh.part[t & 1][warp] = make_float2(sum, sq);
+        }
+      }
+      if (wpr > 1) {
+        row_warps_meet();
+        if (q == 0 && row0 + my_row < hi) {
+          // sum (x - m)^2 = sum (x - m_w)^2 + n_w (m_w - m)^2 over the row's warps w
+          const float2 p = lane < wpr ? sh.part[t & 1][warp + lane] : make_float2(0.0f, 0.0f);
+          const float mean = RMS ? 0.0f : divide_by(warp_sum(p.x), n, inv_n);
+          const float d = RMS ? 0.0f : divide_by(p.x, lane_n, lane_inv) - mean;
+          finish(row0 + my_row, my_row, s, mean, warp_sum(fmaf(lane_n * d, d, p.y)));
+        }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sh.summed[s]));
+      if (lane == 0 && q == 0) mbar_arrive(smem_u32(&sh.summed[s]));
       if (++s == L.slots) {
         s = 0;
         ph ^= 1u;
@@ -709,42 +745,20 @@ __global__ void __launch_bounds__(tile_threads(CW), 1)
         if (!RMS) load_weight2<T, VEC>(b[RMS ? 0 : i], P.bias, P.wf32, col, 0.0f);
       }
     }
-    const float n = static_cast<float>(P.cols), inv_n = 1.0f / n;
-    const int parts = L.rows < kRowWarps ? kRowWarps : L.rows;
-    const int l = lane & (parts - 1);        // lane l merges the tile's l-th sum
-    const float part_n = static_cast<float>(part_vectors(n_vec, wpr, l % wpr) * VEC);
-    const float part_inv = part_n > 0.0f ? 1.0f / part_n : 0.0f;
     for (int t = 0; t < tiles; ++t) {
       const long long row0 = lo + static_cast<long long>(t) * L.rows;
       const int valid = static_cast<int>(hi - row0 < L.rows ? hi - row0 : L.rows);
       tile_wait(&sh.full[s], ph, &sh.abort, status);
       tile_wait(&sh.summed[s], ph, &sh.abort, status);
-      // the rows' statistics, all rows at once over the lanes
-      const float2 p = l / wpr < valid ? sh.part[s][l] : make_float2(0.0f, 0.0f);
-      float mean = 0.0f, m2 = p.y;
-      if (!RMS) {
-        float total = p.x;
-        for (int o = 1; o < wpr; o <<= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-        mean = divide_by(total, n, inv_n);
-        const float d = divide_by(p.x, part_n, part_inv) - mean;
-        m2 += part_n * d * d;
-      }
-      for (int o = 1; o < wpr; o <<= 1) m2 += __shfl_xor_sync(0xffffffffu, m2, o);
-      const float rstd = inv_sqrt(fmaf(m2, inv_n, P.eps));
-      if (warp == kRowWarps && lane < parts && l % wpr == 0 && l / wpr < valid) {
-        if (!RMS && P.mean) P.mean[row0 + l / wpr] = mean;
-        if (P.rstd) P.rstd[row0 + l / wpr] = rstd;
-      }
       uint32_t x = smem_u32(ring) + s * L.slot_bytes + tile_shift<T, VEC>(P, row0) +
                    g * row_bytes + tid * kVecBytes;
       T* y = static_cast<T*>(P.y) + (row0 + g) * P.ldy + tid * VEC;
 #pragma unroll 2
       for (int r0 = 0; r0 < valid; r0 += groups, x += groups * row_bytes, y += groups * P.ldy) {
         const int r = r0 + g;
-        const float row_mean = RMS ? 0.0f : __shfl_sync(0xffffffffu, mean, r * wpr);
-        const float row_rstd = __shfl_sync(0xffffffffu, rstd, r * wpr);
         if (g < groups && r < valid) {
-          const f32x2 shift = make2(-row_mean, -row_mean), scale = make2(row_rstd, row_rstd);
+          const float4 st = sh.stat[s][r];
+          const f32x2 shift = make2(-st.x, -st.x), scale = make2(st.y, st.y);
 #pragma unroll
           for (int i = 0; i < VPT; ++i) {
             const int col = (i * L.group + tid) * VEC;
@@ -809,6 +823,7 @@ __global__ void __launch_bounds__(tile_threads(CW), 1)
   if (warp < kRowWarps) {
     // ---- row warps: their part of the sums of g * (x - mean) and of g
     const int my_row = warp / wpr, q = warp - my_row * wpr;
+    const float inv_n = 1.0f / static_cast<float>(P.cols);
     // lane l holds the statistics of row l of the tile, loaded one tile ahead
     float next_mean = 0.0f, next_rstd = 0.0f;
     auto load_stats = [&](long long row) {
@@ -861,10 +876,26 @@ __global__ void __launch_bounds__(tile_threads(CW), 1)
         float c1 = b1.x + b1.y, c2 = b2.x + b2.y;
         c2 = warp_sum(c2) * rstd;
         if (!RMS) c1 = warp_sum(c1);
-        if (lane == 0) sh.part[s][r * wpr + q] = make_float2(c1, c2);
+        if (lane == 0) {
+          if (wpr == 1)
+            sh.stat[s][r] = make_float4(mean, rstd, c1 * inv_n, c2 * inv_n);
+          else
+            sh.part[t & 1][warp] = make_float2(c1, c2);
+        }
+      }
+      if (wpr > 1) {
+        row_warps_meet();
+        if (q == 0 && row0 + my_row < hi) {
+          const float2 p = lane < wpr ? sh.part[t & 1][warp + lane] : make_float2(0.0f, 0.0f);
+          const float c1 = RMS ? 0.0f : warp_sum(p.x), c2 = warp_sum(p.y);
+          const float mean = RMS ? 0.0f : __shfl_sync(0xffffffffu, means, my_row);
+          const float rstd = __shfl_sync(0xffffffffu, rstds, my_row);
+          if (lane == 0)
+            sh.stat[s][my_row] = make_float4(mean, rstd, c1 * inv_n, c2 * inv_n);
+        }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sh.summed[s]));
+      if (lane == 0 && q == 0) mbar_arrive(smem_u32(&sh.summed[s]));
       if (++s == L.slots) {
         s = 0;
         ph ^= 1u;
@@ -898,45 +929,20 @@ __global__ void __launch_bounds__(tile_threads(CW), 1)
       if (GRADW && !RMS) db[GRADW && !RMS ? i : 0][j] = make2(0.0f, 0.0f);
     }
   }
-  const float inv = 1.0f / static_cast<float>(P.cols);
-  const int parts = L.rows < kRowWarps ? kRowWarps : L.rows;
-  const int l = lane & (parts - 1);
-  // lane l holds the statistics of row l of the tile, loaded one tile ahead
-  float next_mean = 0.0f, next_rstd = 0.0f;
-  auto load_stats = [&](long long row) {
-    if (l < L.rows && row + l < hi) {
-      if (!RMS) next_mean = P.mean[row + l];
-      next_rstd = P.rstd[row + l];
-    }
-  };
-  load_stats(lo);
   for (int t = 0; t < tiles; ++t) {
     const long long row0 = lo + static_cast<long long>(t) * L.rows;
     const int valid = static_cast<int>(hi - row0 < L.rows ? hi - row0 : L.rows);
-    const float mean = next_mean, rstd = next_rstd;
-    load_stats(row0 + L.rows);
     tile_wait(&sh.full[s], ph, &sh.abort, status);
     tile_wait(&sh.summed[s], ph, &sh.abort, status);
-    const float2 p = l / wpr < valid ? sh.part[s][l] : make_float2(0.0f, 0.0f);
-    float c1 = p.x, c2 = p.y;
-    for (int o = 1; o < wpr; o <<= 1) {
-      c2 += __shfl_xor_sync(0xffffffffu, c2, o);
-      if (!RMS) c1 += __shfl_xor_sync(0xffffffffu, c1, o);
-    }
-    c1 *= inv;
-    c2 *= inv;
     uint32_t x = smem_u32(ring) + s * 2 * L.slot_bytes + tile_shift<T, VEC>(P, row0) +
                  g * row_bytes + tid * kVecBytes;
     T* dx = static_cast<T*>(P.y) + (row0 + g) * P.ldy + tid * VEC;
     for (int r0 = 0; r0 < valid; r0 += groups, x += groups * row_bytes, dx += groups * P.ldy) {
       const int r = r0 + g;
-      const float row_mean = RMS ? 0.0f : __shfl_sync(0xffffffffu, mean, r);
-      const float row_rstd = __shfl_sync(0xffffffffu, rstd, r);
-      const float row_c2 = __shfl_sync(0xffffffffu, c2, r * wpr);
-      const float row_c1 = RMS ? 0.0f : __shfl_sync(0xffffffffu, c1, r * wpr);
       if (g < groups && r < valid) {
-        const f32x2 shift = make2(-row_mean, -row_mean), scale = make2(row_rstd, row_rstd);
-        const f32x2 minus_c1 = make2(-row_c1, -row_c1), minus_c2 = make2(-row_c2, -row_c2);
+        const float4 st = sh.stat[s][r];
+        const f32x2 shift = make2(-st.x, -st.x), scale = make2(st.y, st.y);
+        const f32x2 minus_c1 = make2(-st.z, -st.z), minus_c2 = make2(-st.w, -st.w);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
           const int col = (i * L.group + tid) * VEC;
