@@ -1,8 +1,8 @@
-"""Build libmoe_ffn.so in-tree for sm_100a with nvcc.
+"""Build libmoe_ffn.so in-tree for sm_100a with nvcc, and the Python module behind ops.py.
 
 Usage: ``python -m mixture_experts_ffn_expert_b200.build`` (or ``build()``).
-The library lands in ``mixture_experts_ffn_expert_b200/lib/`` next to the
-binding that loads it. nvcc cross-compiles, so no GPU is needed to build.
+The libraries land in ``mixture_experts_ffn_expert_b200/lib/`` next to the
+binding that loads them. nvcc cross-compiles, so no GPU is needed to build.
 """
 from __future__ import annotations
 
@@ -20,6 +20,9 @@ LIBNAME = "libmoe_ffn.so"
 SOURCES = ["moe_ffn.cu", "gated_ffn.cu", "ops.cu"]
 HEADERS = ["ptx_sm100.cuh", "gemm_sm100.cuh", "route.cuh", "router_sm100.cuh",
            "dense_gemm_sm100.cuh", "stream_gemm_sm100.cuh", "norm.cuh", "dropout.cuh", "ops_types.cuh", "ops_host.h"]
+
+HOST_NAME = "_moe_host.so"
+HOST_SOURCE = "host_ops.cpp"
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -40,20 +43,58 @@ def lib_path() -> str:
     return os.path.join(LIBDIR, LIBNAME)
 
 
-def _stale(target: str) -> bool:
+def host_path() -> str:
+    return os.path.join(LIBDIR, HOST_NAME)
+
+
+def _stale(target: str, sources) -> bool:
     if not os.path.exists(target):
         return True
     t = os.path.getmtime(target)
-    deps = [os.path.join(CSRC, s) for s in SOURCES + HEADERS]
+    deps = [os.path.join(CSRC, s) for s in sources]
     deps.append(os.path.join(INCLUDE, "moe_ffn.h"))
     deps.append(os.path.abspath(__file__))
     return any(os.path.getmtime(p) > t for p in deps)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
-    """Compile the CUDA library (skipped when it is newer than its sources)."""
+    """Compile the CUDA library and the module behind ops.py (each skipped when it is newer
+    than its sources). Returns the CUDA library's path."""
+    target = _build_library(force, verbose, extra_flags)
+    _build_host(force, verbose)
+    return target
+
+
+def _build_host(force: bool, verbose: bool) -> None:
+    """The torch-facing module: plain C++ against torch's headers, linked to the library."""
+    target = host_path()
+    if not force and not _stale(target, [HOST_SOURCE]):
+        return
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    tmp = target + ".tmp"
+    torch_lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cuda_include = os.path.join(os.path.dirname(os.path.dirname(nvcc_path())), "include")
+    includes = [INCLUDE, *cpp_extension.include_paths(), sysconfig.get_paths()["include"],
+                cuda_include]
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[f"-I{i}" for i in includes], os.path.join(CSRC, HOST_SOURCE), "-o", tmp,
+           f"-L{LIBDIR}", f"-l:{LIBNAME}", "-Wl,-rpath,$ORIGIN", f"-L{torch_lib}",
+           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed ({res.returncode}):\n{res.stdout}\n{res.stderr}")
+    os.replace(tmp, target)
+
+
+def _build_library(force: bool, verbose: bool, extra_flags) -> str:
     target = lib_path()
-    if not force and not _stale(target):
+    if not force and not _stale(target, SOURCES + HEADERS):
         return target
     os.makedirs(LIBDIR, exist_ok=True)
     tmp = target + ".tmp"

@@ -200,3 +200,10 @@ def test_cpu_tensors_are_refused():
                  lambda: ops.dropout_add_backward(x, 0.1, None)):
         with pytest.raises(MoEError):
             call()
+
+
+def test_missing_module_fails_loudly(monkeypatch, tmp_path):
+    monkeypatch.setattr(ops, "_MODULE", None)
+    monkeypatch.setattr(ops, "host_path", lambda: str(tmp_path / "nope.so"))
+    with pytest.raises(MoEError):
+        ops.norm_forward(torch.zeros(4, 64))
