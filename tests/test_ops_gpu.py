@@ -654,6 +654,24 @@ def test_training_step_in_a_graph_and_on_other_streams():
     ops.device_status()
 
 
+@pytest.mark.parametrize("seed", range(24))
+def test_random_shapes(seed):
+    """Seeded shapes over the whole range of each operator (sizes log-uniform, odd ones
+    among them), with the bounds of the fixed cases."""
+    import random
+    r = random.Random(seed)
+    log = lambda lo, hi: int(round(math.exp(r.uniform(math.log(lo), math.log(hi)))))  # noqa: E731
+    d, f = 8 * log(1, 160), 8 * log(1, 160)
+    check_ffn(log(1, 1500), d, f, r.choice(["bf16", "fp16"]), r.choice(["silu", "gelu"]), seed)
+    for _ in range(3):
+        cols = log(1, 12000)
+        rows = log(1, max(1, min(4000, 3_000_000 // cols)))
+        test_norm(rows, cols, *r.choice([("bf16", "bf16"), ("bf16", "fp32"), ("fp16", "fp16"),
+                                         ("fp32", "fp32")]), r.choice(["layer", "rms"]))
+        test_dropout_add(rows, cols, r.choice(["bf16", "fp16", "fp32"]),
+                         r.choice([0.0, 0.1, 0.37, 0.9]))
+
+
 FIRST_CALL = """
 import torch
 from mixture_experts_ffn_expert_b200 import ops
