@@ -189,6 +189,7 @@ cudaError_t launch(GemmLaunch& L, const DeviceInfo& d, cudaStream_t st) {
 
 template <int EPI>
 cudaError_t launch_any(GemmLaunch& L, bool pair, const DeviceInfo& d, cudaStream_t st) {
+  if (!L.ok) return cudaErrorInvalidValue;         // a tensor map could not be encoded
   if (L.half)
     return pair ? launch<__half, EPI, true>(L, d, st) : launch<__half, EPI, false>(L, d, st);
   return pair ? launch<__nv_bfloat16, EPI, true>(L, d, st)
@@ -198,7 +199,7 @@ cudaError_t launch_any(GemmLaunch& L, bool pair, const DeviceInfo& d, cudaStream
 // How a product of `tokens` rows, `n` columns (of one of gate / up) and `kb` k-blocks runs:
 // on CTA pairs, on single CTAs, or streaming its weights with a split reduction. Estimates in
 // microseconds, from measurements on B200: a k-block of 64 takes about 0.3 us in a 256 x 256
-// tile of a pair, 0.21 in a 128 x 128 tile of one CTA (the rate at which MMAs are issued),
+// tile of a pair, 0.21 in a 128 x 128 tile of one CTA (32 KB of operands from L2 an SM),
 // and the split reduction ends with about 3.5 us of exchange more. Up to 128 tokens the
 // weights are streamed in any case.
 enum Shape { kPairs, kSingle, kStream };
@@ -259,7 +260,7 @@ cudaError_t launch_stream_columns(StreamLaunch& L, const DeviceInfo& d, cudaStre
 
 template <int EPI>
 cudaError_t launch_stream(StreamLaunch& L, const DeviceInfo& d, cudaStream_t st) {
-  if (!L.ok) return cudaErrorInvalidValue;
+  if (!L.ok) return cudaErrorInvalidValue;         // a tensor map could not be encoded
   const int nb = L.columns();
   if (L.half) {
     if (nb == 16) return launch_stream_columns<__half, EPI, 16>(L, d, st);
