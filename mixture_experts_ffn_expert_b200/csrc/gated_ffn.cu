@@ -201,7 +201,7 @@ cudaError_t launch_any(GemmLaunch& L, bool pair, const DeviceInfo& d, cudaStream
 // microseconds, from measurements on B200: a k-block of 64 takes about 0.3 us in a 256 x 256
 // tile of a pair, 0.21 in a 128 x 128 tile of one CTA (32 KB of operands from L2 an SM),
 // and the split reduction ends with about 3.5 us of exchange more. Up to 128 tokens the
-// weights are streamed in any case.
+// weights are streamed, small forwards of more than 64 excepted (small_forward).
 enum Shape { kPairs, kSingle, kStream };
 
 int stream_ranks(int64_t tiles, int64_t kb, int sms) {
@@ -228,6 +228,22 @@ Shape choose(int64_t tokens, int64_t n, int64_t kb, bool glu, const DeviceInfo& 
   const double stream = ceil_div(t128 * ranks, d.sms) * ceil_div(kb, ranks) * 0.21 + 3.5;
   if (stream < pairs && stream < single) return kStream;
   return pairs <= single ? kPairs : kSingle;
+}
+
+// Whether a forward over 65 to 128 tokens runs on single CTAs: its matrices are so small that
+// the exchange after both split reductions, 0.045 us a token each, costs more than they save
+// (128 tokens, d=f=1024: 13.9 us, 17.1 streamed; d=7168, f=2048: 43.9 and 36.6).
+bool small_forward(int64_t tokens, int64_t d, int64_t f, const DeviceInfo& dev) {
+  if (tokens <= 64 || tokens > moe::kStreamTokens) return false;
+  double single = 0.0, stream = 0.0;
+  const int64_t shape[2][2] = {{2 * f, d}, {d, f}};        // columns and reduction
+  for (const auto& s : shape) {
+    const int64_t tiles = ceil_div(s[0], 128), kb = ceil_div(s[1], 64);
+    const int ranks = stream_ranks(tiles, kb, dev.sms);
+    single += ceil_div(tiles, dev.sms) * kb * 0.21;
+    stream += ceil_div(tiles * ranks, dev.sms) * ceil_div(kb, ranks) * 0.21 + 0.045 * tokens;
+  }
+  return single < stream;
 }
 
 // One product whose weights are streamed by clusters that split the reduction until there
@@ -346,7 +362,8 @@ int moe_gated_ffn_forward(int act, int dtype, int64_t T, int64_t d, int64_t f, c
   const int half = dtype == MOE_DTYPE_FP16;
   cudaError_t e;
   bool overlapped = false;       // the first kernel lets the second load weights early
-  const Shape first = choose(T, f, ceil_div(d, 64), true, *dev);
+  const bool small = small_forward(T, d, f, *dev);
+  const Shape first = small ? kSingle : choose(T, f, ceil_div(d, 64), true, *dev);
   if (first == kStream) {
     StreamLaunch L;
     L.half = half;
@@ -378,7 +395,7 @@ int moe_gated_ffn_forward(int act, int dtype, int64_t T, int64_t d, int64_t f, c
     e = launch_any<moe::kGemmGluForward>(L, pair, *dev, st);
   }
   if (e != cudaSuccess) return cuda_error(e, "gated feed-forward gate/up launch");
-  const Shape second = choose(T, d, ceil_div(f, 64), false, *dev);
+  const Shape second = small ? kSingle : choose(T, d, ceil_div(f, 64), false, *dev);
   if (second == kStream) {
     StreamLaunch L;
     L.half = half;
