@@ -591,9 +591,10 @@ __device__ __forceinline__ void tile_producer(const NormParams& P, const NormTil
                                               TileShared& sh, long long lo, long long hi, int tiles,
                                               int* status) {
   int s = 0;
-  uint32_t ph = 0;
+  uint32_t ph = 0, issued = 0, last = 0;           // slots in use, parity of their last copy
   for (int t = 0; t < tiles; ++t) {
     tile_wait(&sh.free[s], ph ^ 1u, &sh.abort, status);
+    if (*static_cast<volatile int*>(&sh.abort)) break;
     const long long row = lo + static_cast<long long>(t) * L.rows;
     const int n = static_cast<int>(hi - row < L.rows ? hi - row : L.rows);
     uint8_t* slot = ring + static_cast<size_t>(s) * PLANES * L.slot_bytes;
@@ -605,11 +606,19 @@ __device__ __forceinline__ void tile_producer(const NormParams& P, const NormTil
     tile_copy<T, VEC, true>(P, L, P.x, P.ldx, row, n, slot, bar);
     if (PLANES == 2)
       tile_copy<T, VEC, true>(P, L, P.dy, P.lddy, row, n, slot + L.slot_bytes, bar);
+    issued |= 1u << s;
+    last = (last & ~(1u << s)) | (ph << s);
     if (++s == L.slots) {
       s = 0;
       ph ^= 1u;
     }
   }
+  // the block keeps its shared memory until the copies have landed, given up or not
+  for (int i = 0; i < L.slots; ++i)
+    if (issued >> i & 1u) {
+      int never = 0;
+      tile_wait(&sh.full[i], last >> i & 1u, &never, status);
+    }
 }
 
 __device__ __forceinline__ void tile_init(const NormTile& L, TileShared& sh, int column_warps) {
