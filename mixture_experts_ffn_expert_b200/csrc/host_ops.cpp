@@ -54,6 +54,7 @@ const at::Tensor& cuda_tensor(PyObject* o, const char* what) {
   const at::Tensor& t = THPVariable_Unpack(o);
   if (!t.is_cuda() || t.layout() != at::kStrided)
     refuse(std::string(what) + " must be a CUDA tensor");
+  if (t.is_neg()) refuse(std::string(what) + " is a lazily negated view: call resolve_neg()");
   return t;
 }
 

@@ -754,3 +754,15 @@ def test_same_tensor_twice():
     got = ops.dropout_add_forward(x, x, 0.25, rng)
     want = O.dropout_add(f64(x), f64(x), 0.25, 3, 4)
     close(got, want, drop_tol(f64(x), f64(x), 0.25, torch.bfloat16, want), "x twice")
+
+
+def test_negated_views_are_refused_or_resolved():
+    # a view with torch's negative bit holds the unnegated values in memory
+    x = randn(gen(32), 6, 64, dtype=torch.float32)
+    neg = torch._neg_view(x)
+    rng = torch.tensor([5, 6], device="cuda")
+    for call in (lambda: ops.norm_forward(neg), lambda: ops.dropout_add_forward(neg, x, 0.5, rng),
+                 lambda: ops.dropout_add_forward(x, neg, 0.5, rng)):
+        with pytest.raises(MoEError):
+            call()
+    assert torch.equal(ops.norm_forward(neg.resolve_neg()), ops.norm_forward(-x))
