@@ -105,14 +105,20 @@ class _Norm(torch.autograd.Function):
         return dx, dw, db, None, None
 
 
+def _norm(x, weight, bias, eps, kind):
+    if not torch.is_grad_enabled():      # nothing to save (autograd asks the inputs alone)
+        return norm_forward(x, weight, bias, eps, kind)
+    return _Norm.apply(x, weight, bias, eps, kind)
+
+
 def layer_norm(x, weight=None, bias=None, eps: float = 1e-5) -> torch.Tensor:
     """Differentiable layer norm over x's last dimension (see ``norm_forward``)."""
-    return _Norm.apply(x, weight, bias, eps, "layer")
+    return _norm(x, weight, bias, eps, "layer")
 
 
 def rms_norm(x, weight=None, eps: float = 1e-5) -> torch.Tensor:
     """Differentiable RMS norm over x's last dimension (see ``norm_forward``)."""
-    return _Norm.apply(x, weight, None, eps, "rms")
+    return _norm(x, weight, None, eps, "rms")
 
 
 # ------------------------------------------------------------------------ gated feed-forward
@@ -157,6 +163,8 @@ class _GatedFFN(torch.autograd.Function):
 
 def gated_ffn(x, W1, W3, W2, activation: str = "silu") -> torch.Tensor:
     """Differentiable gated feed-forward block (see ``gated_ffn_forward``)."""
+    if not torch.is_grad_enabled():
+        return gated_ffn_forward(x, W1, W3, W2, activation)
     return _GatedFFN.apply(x, W1, W3, W2, activation)
 
 
@@ -199,6 +207,8 @@ class _DropoutAdd(torch.autograd.Function):
 def dropout_add(x, residual, p: float, rng: Optional[torch.Tensor]) -> torch.Tensor:
     """Differentiable residual + dropout(x) (see ``dropout_add_forward``). rng must hold the
     same seed and offset in the backward pass: changing it in place in between raises."""
+    if not torch.is_grad_enabled():
+        return dropout_add_forward(x, residual, p, rng)
     return _DropoutAdd.apply(x, residual, p, rng)
 
 
@@ -208,7 +218,7 @@ def gated_ffn_block(x, W1, W3, W2, norm_weight=None, norm_bias=None, norm: str =
     """Differentiable pre-norm residual block x + dropout(gated_ffn(norm(x))): the block
     around the layer ("Shared Expert (DeepSeek-V3)", "How it works": normalised input, the
     residual added at block level) with a dense feed-forward layer in its middle."""
-    h = _Norm.apply(x, norm_weight, norm_bias, eps, norm)
+    h = _norm(x, norm_weight, norm_bias, eps, norm)
     return dropout_add(gated_ffn(h, W1, W3, W2, activation), x, p, rng)
 
 

@@ -756,6 +756,31 @@ def test_same_tensor_twice():
     close(got, want, drop_tol(f64(x), f64(x), 0.25, torch.bfloat16, want), "x twice")
 
 
+def test_no_grad_saves_nothing():
+    # leaves that want gradients under no_grad: the forward's bits, and no pre-activations
+    T, d, f = 520, 136, 4096
+    x, W1, W3, W2, _ = ffn_case(T, d, f, "bf16", 31)
+    rng = torch.tensor([5, 6], device="cuda")
+    want = ops.gated_ffn_forward(x, W1, W3, W2)
+    norm = ops.norm_forward(x, kind="rms")
+    drop = ops.dropout_add_forward(want, x, 0.25, rng)
+    block = ops.gated_ffn_block(x, W1, W3, W2, p=0.25, rng=rng)
+    for t in (x, W1, W3, W2):
+        t.requires_grad_(True)
+    with torch.no_grad():
+        before = torch.cuda.memory_allocated()
+        torch.cuda.reset_peak_memory_stats()
+        out = ops.gated_ffn(x, W1, W3, W2)
+        peak = torch.cuda.max_memory_allocated() - before
+        assert torch.equal(ops.rms_norm(x), norm)
+        assert torch.equal(ops.dropout_add(out, x, 0.25, rng), drop)
+        again = ops.gated_ffn_block(x, W1, W3, W2, p=0.25, rng=rng)
+    assert torch.equal(out, want) and not out.requires_grad
+    assert torch.equal(again, block) and not again.requires_grad
+    # act(gate) * up (T, f) and the output; gate and up would be two more of the first
+    assert peak < 2 * (T * f * 2)
+
+
 def test_negated_views_are_refused_or_resolved():
     # a view with torch's negative bit holds the unnegated values in memory
     x = randn(gen(32), 6, 64, dtype=torch.float32)
