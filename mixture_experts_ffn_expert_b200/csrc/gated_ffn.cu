@@ -232,7 +232,9 @@ Shape choose(int64_t tokens, int64_t n, int64_t kb, bool glu, const DeviceInfo& 
 
 // Whether a forward over 65 to 128 tokens runs on single CTAs: its matrices are so small that
 // the exchange after both split reductions, 0.045 us a token each, costs more than they save
-// (128 tokens, d=f=1024: 13.9 us, 17.1 streamed; d=7168, f=2048: 43.9 and 36.6).
+// (128 tokens, d=f=1024: 13.9 us, 17.1 streamed; d=7168, f=2048: 43.9 and 36.6). The estimate
+// must be 1 us ahead: where the two come out equal, streaming is the faster (128 tokens, d=2048,
+// f=2816: 25.7 us, 23.7 streamed).
 bool small_forward(int64_t tokens, int64_t d, int64_t f, const DeviceInfo& dev) {
   if (tokens <= 64 || tokens > moe::kStreamTokens) return false;
   double single = 0.0, stream = 0.0;
@@ -243,7 +245,7 @@ bool small_forward(int64_t tokens, int64_t d, int64_t f, const DeviceInfo& dev) 
     single += ceil_div(tiles, dev.sms) * kb * 0.21;
     stream += ceil_div(tiles * ranks, dev.sms) * ceil_div(kb, ranks) * 0.21 + 0.045 * tokens;
   }
-  return single < stream;
+  return single + 1.0 < stream;
 }
 
 // One product whose weights are streamed by clusters that split the reduction until there
