@@ -10,9 +10,13 @@
 // Both passes are to be bound by memory: the forward reads x and writes y, the backward
 // reads x and dy and writes dx, once each. A row is held in registers (few rows) or shared
 // memory (many) between its statistics and its output; only rows too long for either are
-// read again. Statistics, products and sums are fp32; the variance is the mean of
-// squared differences from the mean (not a difference of two large sums). Results are
-// rounded once, on the store. No atomics: the weight's gradient is summed per thread
+// read again. Statistics, products and sums are fp32. The mean is summed as differences
+// from the row's first element, p: mean = p + sum(x - p) / cols. A sum of the elements
+// themselves is off by several steps of a large mean, and of a constant row of 123456.79 made
+// 0.93 instead of 0; the differences' sum is off by parts of the row's spread only, so the
+// mean is, but for that, the nearest fp32 value. The variance is the mean of squared
+// differences from the mean (not a difference of two large sums). Results are rounded once,
+// on the store. No atomics: the weight's gradient is summed per thread
 // over the rows a block walks, then over the blocks in a fixed order, so equal inputs
 // give equal bits.
 #pragma once
@@ -73,6 +77,12 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
+// The value that a row's elements are taken from while its mean is summed: its first element
+// (0 where that is no number, so that the mean of a row with an infinity is what its sum says).
+__device__ __forceinline__ float row_pivot(float first) {
+  return isfinite(first) ? first : 0.0f;
+}
+
 // Sum over the `threads` threads of one row group (a multiple of 32; named barrier
 // `bar`). `slot` holds one float a warp and is used once per barrier, so two calls in a
 // row take two slots.
@@ -110,15 +120,16 @@ __global__ void __launch_bounds__(1024) norm_forward_kernel(const NormParams P, 
   float mean = 0.0f;
   const float n = static_cast<float>(P.cols);
   if (!P.rms) {
+    const float pivot = row_pivot(to_f32(x[0]));
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int col = (i * group + tid) * VEC;
       if (col < P.cols) {
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) sum += to_f32(a[i].v[j]);
+        for (int j = 0; j < VEC; ++j) sum += to_f32(a[i].v[j]) - pivot;
       }
     }
-    mean = group_sum(sum, s_sum[0], warp, group, 1) / n;
+    mean = pivot + group_sum(sum, s_sum[0], warp, group, 1) / n;
   }
   float sq = 0.0f;
 #pragma unroll
@@ -168,8 +179,9 @@ __global__ void __launch_bounds__(1024) norm_forward_long_kernel(const NormParam
     float mean = 0.0f;
     if (!P.rms) {
       float sum = 0.0f;
-      for (int c = threadIdx.x; c < P.cols; c += blockDim.x) sum += to_f32(x[c]);
-      mean = group_sum(sum, s_sum[0], warp, blockDim.x, 1) / n;
+      const float pivot = row_pivot(to_f32(x[0]));
+      for (int c = threadIdx.x; c < P.cols; c += blockDim.x) sum += to_f32(x[c]) - pivot;
+      mean = pivot + group_sum(sum, s_sum[0], warp, blockDim.x, 1) / n;
     }
     float sq = 0.0f;
     for (int c = threadIdx.x; c < P.cols; c += blockDim.x) {
@@ -528,6 +540,13 @@ __device__ __forceinline__ void ld_tile(f32x2 (&f)[pairs<VEC>()], uint32_t addr)
     }
   }
 }
+// The pivot of the row that starts at a shared-memory address.
+template <typename T>
+__device__ __forceinline__ float tile_pivot(uint32_t row) {
+  f32x2 first[1];
+  ld_tile<T, 1>(first, row);
+  return row_pivot(first[0].x);
+}
 template <typename T, int VEC>
 __device__ __forceinline__ void st_out(T* p, const f32x2 (&f)[pairs<VEC>()]) {
   if constexpr (VEC == 1) {
@@ -563,13 +582,6 @@ __device__ __forceinline__ void tile_range(const NormParams& P, long long* lo, l
   *hi = P.rows * (blockIdx.x + 1) / gridDim.x;
 }
 
-// a / n for a count n with its rounded reciprocal: one Newton step on the quotient gives the
-// division's result (a constant row must have exactly its value as its mean) at the cost of
-// three instructions.
-__device__ __forceinline__ float divide_by(float a, float n, float inv_n) {
-  const float q = a * inv_n;
-  return fmaf(fmaf(-q, n, a), inv_n, q);
-}
 // 1 / sqrt(v), v > 0 (or 0: infinity): the hardware's approximation, refined once.
 __device__ __forceinline__ float inv_sqrt(float v) {
   const float y = rsqrtf(v);
@@ -656,10 +668,11 @@ __global__ void __launch_bounds__(tile_threads(CW), 1)
   if (warp == kRowWarps + CW) {
     if (lane == 0) tile_producer<T, VEC, 1>(P, L, ring, sh, lo, hi, tiles, status);
   } else if (warp < kRowWarps) {
-    // ---- row warps: the sum of this warp's part of its row, and the squared differences
-    // from the part's own mean
+    // ---- row warps: the sum of this warp's part of its row (as differences from the row's
+    // pivot), and the squared differences from the part's own mean. Sums are multiplied by
+    // the counts' reciprocals: being differences, they need no exact division.
     const int my_row = warp / wpr, q = warp - my_row * wpr;
-    const float n = static_cast<float>(P.cols), inv_n = 1.0f / n;
+    const float inv_n = 1.0f / static_cast<float>(P.cols);
     const float own_n = static_cast<float>(part_vectors(n_vec, wpr, q) * VEC);
     const float own_inv = own_n > 0.0f ? 1.0f / own_n : 0.0f;
     // the elements that the warp lane / q' of this row sums (lane < wpr)
@@ -682,23 +695,26 @@ __global__ void __launch_bounds__(tile_threads(CW), 1)
     for (int t = 0; t < tiles; ++t) {
       const long long row0 = lo + static_cast<long long>(t) * L.rows;
       tile_wait(&sh.full[s], ph, &sh.abort, status);
+      float pivot = 0.0f;
       for (int r = my_row; r < L.rows && row0 + r < hi; r += kRowWarps) {
         const uint32_t x = base + s * L.slot_bytes + tile_shift<T, VEC>(P, row0) + r * row_bytes;
         float sum = 0.0f, part_mean = 0.0f;
         if (!RMS) {
+          pivot = tile_pivot<T>(x - (q * 32 + lane) * kVecBytes);
+          const f32x2 from = make2(-pivot, VEC == 1 ? 0.0f : -pivot);
           f32x2 acc[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
           auto add = [&](int k) {
             f32x2 a[kPairs];
             ld_tile<T, VEC>(a, x + k * step);
 #pragma unroll
-            for (int j = 0; j < kPairs; ++j) acc[j & 1] = add2(acc[j & 1], a[j]);
+            for (int j = 0; j < kPairs; ++j) acc[j & 1] = add2(acc[j & 1], add2(a[j], from));
           };
 #pragma unroll 4
           for (int k = 0; k < rounds - 1; ++k) add(k);
           if (last) add(rounds - 1);
           const f32x2 both = add2(acc[0], acc[1]);
           sum = warp_sum(both.x + both.y);
-          part_mean = divide_by(sum, own_n, own_inv);
+          part_mean = fmaf(sum, own_inv, pivot);
         }
         const f32x2 shift = make2(-part_mean, VEC == 1 ? 0.0f : -part_mean);
         f32x2 acc[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
@@ -726,11 +742,13 @@ __global__ void __launch_bounds__(tile_threads(CW), 1)
       if (wpr > 1) {
         row_warps_meet();
         if (q == 0 && row0 + my_row < hi) {
-          // sum (x - m)^2 = sum (x - m_w)^2 + n_w (m_w - m)^2 over the row's warps w
+          // sum (x - m)^2 = sum (x - m_w)^2 + n_w (m_w - m)^2 over the row's warps w; both
+          // means less the pivot
           const float2 p = lane < wpr ? sh.part[t & 1][warp + lane] : make_float2(0.0f, 0.0f);
-          const float mean = RMS ? 0.0f : divide_by(warp_sum(p.x), n, inv_n);
-          const float d = RMS ? 0.0f : divide_by(p.x, lane_n, lane_inv) - mean;
-          finish(row0 + my_row, my_row, s, mean, warp_sum(fmaf(lane_n * d, d, p.y)));
+          const float off = RMS ? 0.0f : warp_sum(p.x) * inv_n;
+          const float d = RMS ? 0.0f : p.x * lane_inv - off;
+          // (this warp's pivot is that of row my_row, the only row it summed)
+          finish(row0 + my_row, my_row, s, off + pivot, warp_sum(fmaf(lane_n * d, d, p.y)));
         }
       }
       __syncwarp();

@@ -1,0 +1,60 @@
+"""GPU edge cases of the norm, gated feed-forward and dropout operators: what the shapes and
+values of the general tests do not reach. Bounds and helpers are those of the general tests
+(u: half a step of a type, U32 = 2^-24)."""
+import numpy as np
+import pytest
+import torch
+
+from mixture_experts_ffn_expert_b200 import ops
+from oracle import ops_oracle as O
+from test_ops_gpu import DT, K, U32, close, f64, gen, randn
+
+pytestmark = pytest.mark.gpu
+
+# Rows and columns that reach every norm kernel: a warp and a block a row, aligned and not;
+# tiles of many and of few rows, aligned and not; rows too long for registers.
+NORM_KERNELS = [(5, 32), (3, 1000), (3, 1003), (2, 7168), (3, 70000), (700, 24), (700, 128),
+                (700, 1000), (700, 1003), (700, 7168), (700, 7001), (1300, 16384), (601, 70000)]
+
+
+# ------------------------------------------------------------------------ norm
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("rows,cols", NORM_KERNELS)
+def test_constant_rows_have_their_value_as_mean(rows, cols, dtype):
+    dt = DT[dtype]
+    values = torch.tensor([1000.1, 123456.79, -0.1, 987.654, 1e8, 3.3, -1017.77, 0.0])
+    if dtype == "fp16":
+        values = values.clamp(-60000, 60000)
+    v = values.to(dt).repeat((rows + 7) // 8)[:rows].cuda()
+    x = v[:, None].expand(rows, cols).contiguous()
+    b = randn(gen(1), cols, dtype=dt)
+    y, mean, rstd = ops.norm_forward(x, None, b, save=True)
+    assert torch.equal(mean, v.float())
+    assert torch.equal(y, b.expand_as(y))
+    # sqrt, division and eps itself: three roundings
+    assert (rstd.double() * 1e-5 ** 0.5 - 1).abs().max().item() <= 4 * U32
+
+
+@pytest.mark.parametrize("rows,cols", NORM_KERNELS)
+def test_nearly_constant_rows(rows, cols):
+    # Rows of a value plus 0 to 3 steps of it. The mean that a kernel may use is fp32: off by
+    # half a step of it, U32 |mean|, and by its sum's error, relative to the rows' spread only.
+    # It moves y by rstd times that, and the variance by its square.
+    g = gen(rows + cols)
+    values = torch.tensor([1000.1, 123456.79, -987.654, 33333.3]).repeat((rows + 3) // 4)[:rows]
+    step = torch.from_numpy(np.spacing(np.abs(values.numpy())))
+    x = values[:, None] + step[:, None] * torch.randint(0, 4, (rows, cols), generator=g)
+    assert x.dtype == torch.float32
+    y, mean, rstd = (f64(t) for t in ops.norm_forward(x.cuda(), save=True))
+    x = x.double().numpy()
+    want, m, r = O.norm(x)
+    spread = x.max(1) - x.min(1)
+    e = U32 * np.abs(m) * (1 + 2 * U32) + K * U32 * spread
+    assert (np.abs(mean - m) <= e).all()
+    # |d rstd| <= rstd^3 / 2 times the variance's error: e^2, and K U32 of the variance
+    var = 1 / r ** 2 - 1e-5
+    er = (e ** 2 + K * U32 * var) / (2 * (var + 1e-5)) + 4 * U32
+    assert (np.abs(rstd / r - 1) <= er).all()
+    xh = np.abs(want)
+    tol = (r * e * (1 + er))[:, None] + xh * (er + 4 * U32)[:, None] + U32 * xh
+    close(y, want, tol, "y")
