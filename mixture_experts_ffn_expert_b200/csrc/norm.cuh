@@ -188,7 +188,9 @@ __global__ void __launch_bounds__(1024) norm_forward_long_kernel(const NormParam
       const float v = to_f32(x[c]) - mean;
       sq += v * v;
     }
-    const float rstd = 1.0f / sqrtf(group_sum(sq, s_sum[1], warp, blockDim.x, 1) / n + P.eps);
+    // divided before the threads' sums meet: the sum of a long row's squares may pass fp32's
+    // range where their mean does not
+    const float rstd = 1.0f / sqrtf(group_sum(sq / n, s_sum[1], warp, blockDim.x, 1) + P.eps);
     if (threadIdx.x == 0) {
       if (P.mean) P.mean[row] = mean;
       if (P.rstd) P.rstd[row] = rstd;

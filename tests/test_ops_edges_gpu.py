@@ -58,3 +58,18 @@ def test_nearly_constant_rows(rows, cols):
     xh = np.abs(want)
     tol = (r * e * (1 + er))[:, None] + xh * (er + 4 * U32)[:, None] + U32 * xh
     close(y, want, tol, "y")
+
+
+@pytest.mark.parametrize("kind", ["layer", "rms"])
+@pytest.mark.parametrize("rows,cols", NORM_KERNELS)
+def test_inverse_deviation_over_the_range(rows, cols, kind):
+    # no eps: rows of any size from 1e-17 to 1e17, whose squares neither overflow nor leave
+    # fp32's normal numbers; a statistic is off by K U32, the root and the division by 2 U32
+    g = gen(rows + 3 * cols)
+    scale = 10.0 ** (34.0 * torch.rand((rows, 1), generator=g) - 17.0)
+    x = (torch.randn((rows, cols), generator=g) * scale).cuda()
+    y, mean, rstd = ops.norm_forward(x, eps=0.0, kind=kind, save=True)
+    want, m, r = O.norm(f64(x), eps=0.0, kind=kind)
+    assert (np.abs(f64(rstd) / r - 1) <= K * U32).all()
+    biggest = np.abs(f64(x)).max(axis=1, keepdims=True) if kind == "layer" else 0.0
+    close(y, want, K * U32 * (np.abs(want) + r[:, None] * biggest), "y")
