@@ -584,7 +584,10 @@ __device__ __forceinline__ void tile_range(const NormParams& P, long long* lo, l
   *hi = P.rows * (blockIdx.x + 1) / gridDim.x;
 }
 
-// 1 / sqrt(v), v > 0 (or 0: infinity): the hardware's approximation, refined once.
+// 1 / sqrt(v), v > 0 (or 0: infinity): rsqrtf (off by at most 2 units in the last place) and one
+// step of Newton's method on f(y) = 1 / y^2 - v, y' = y + y (1 - v y^2) / 2, whose own roundings
+// then count: at most 4 * 2^-24 in all. The step is left out where v y y could leave the normal
+// numbers. (1.0f / sqrtf(v) in its place: 16384 x 128 bf16 RMS forward 8.5 us instead of 7.7.)
 __device__ __forceinline__ float inv_sqrt(float v) {
   const float y = rsqrtf(v);
   const float e = fmaf(-0.5f * v * y, y, 0.5f);

@@ -73,3 +73,18 @@ def test_inverse_deviation_over_the_range(rows, cols, kind):
     assert (np.abs(f64(rstd) / r - 1) <= K * U32).all()
     biggest = np.abs(f64(x)).max(axis=1, keepdims=True) if kind == "layer" else 0.0
     close(y, want, K * U32 * (np.abs(want) + r[:, None] * biggest), "y")
+
+
+@pytest.mark.parametrize("rows,cols", [(3, 512), (3, 4096), (700, 128), (700, 1024), (1300, 512),
+                                       (5000, 64), (2, 1 << 17)])
+def test_inverse_root_of_exact_mean_squares(rows, cols):
+    # rows of +-a, a of 8 bits: every sum of their squares is exact (a power of two of 16-bit
+    # numbers), so the inverse deviation shows the root's and the division's roundings alone
+    g = gen(rows + 7 * cols)
+    a = torch.randint(128, 256, (rows, 1), generator=g) * \
+        2.0 ** torch.randint(-60, 50, (rows, 1), generator=g)
+    sign = 1 - 2 * torch.randint(0, 2, (rows, cols), generator=g)
+    x = (a * sign).bfloat16().cuda()
+    assert torch.equal(x.float().cpu().abs(), a.float().expand(rows, cols))
+    rstd = f64(ops.norm_forward(x, eps=0.0, kind="rms", save=True)[2])
+    assert np.abs(rstd * f64(a)[:, 0] - 1).max() <= 4 * U32
