@@ -55,6 +55,10 @@ const at::Tensor& cuda_tensor(PyObject* o, const char* what) {
   if (!t.is_cuda() || t.layout() != at::kStrided)
     refuse(std::string(what) + " must be a CUDA tensor");
   if (t.is_neg()) refuse(std::string(what) + " is a lazily negated view: call resolve_neg()");
+  // The C ABI reads a null pointer as an argument that was not given. A wrapper subclass or a
+  // fake tensor says it is on the device and has none of its memory.
+  if (!t.has_storage() || (t.numel() > 0 && !t.storage().data()))
+    refuse(std::string(what) + " has no memory of its own (a wrapper or a fake tensor)");
   return t;
 }
 

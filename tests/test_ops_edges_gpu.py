@@ -6,8 +6,10 @@ import pytest
 import torch
 
 from mixture_experts_ffn_expert_b200 import ops
+from mixture_experts_ffn_expert_b200.binding import MoEError
 from oracle import ops_oracle as O
-from test_ops_gpu import DT, K, U32, close, f64, gen, randn
+from test_ops_edges_cpu import Wrapper
+from test_ops_gpu import DT, K, U32, close, f64, ffn_case, gen, randn
 
 pytestmark = pytest.mark.gpu
 
@@ -88,3 +90,30 @@ def test_inverse_root_of_exact_mean_squares(rows, cols):
     assert torch.equal(x.float().cpu().abs(), a.float().expand(rows, cols))
     rstd = f64(ops.norm_forward(x, eps=0.0, kind="rms", save=True)[2])
     assert np.abs(rstd * f64(a)[:, 0] - 1).max() <= 4 * U32
+
+
+# ------------------------------------------------------------------------ arguments
+def test_an_argument_without_memory_is_not_an_absent_one():
+    x, W1, W3, W2, dout = ffn_case(8, 64, 72, "bf16", 40)
+    out, gate, up = ops.gated_ffn_forward(x, W1, W3, W2, save=True)
+    y, mean, rstd = ops.norm_forward(x, save=True)
+    w = torch.ones(64, device="cuda")
+    rng = torch.tensor([1, 2], device="cuda")
+    wrap = lambda t: Wrapper(t, t.device)                                  # noqa: E731
+    calls = [lambda: ops.norm_forward(x, wrap(w)), lambda: ops.norm_forward(x, w, wrap(w)),
+             lambda: ops.norm_forward(x, None, wrap(w)),
+             lambda: ops.norm_backward(dout, x, wrap(w), mean, rstd),
+             lambda: ops.norm_backward(wrap(dout), x, w, mean, rstd),
+             lambda: ops.norm_backward(dout, x, w, wrap(mean), rstd),
+             lambda: ops.norm_backward(dout, x, w, mean, wrap(rstd)),
+             lambda: ops.dropout_add_forward(x, wrap(dout), 0.1, rng),
+             lambda: ops.dropout_add_forward(x, wrap(dout), 0.0, None),
+             lambda: ops.dropout_add_forward(x, dout, 0.1, wrap(rng)),
+             lambda: ops.gated_ffn_forward(x, wrap(W1), W3, W2),
+             lambda: ops.gated_ffn_forward(x, W1, W3, wrap(W2)),
+             lambda: ops.gated_ffn_backward(dout, x, W1, W3, W2, wrap(gate), up),
+             lambda: ops.gated_ffn_backward(wrap(dout), x, W1, W3, W2, gate, up)]
+    for i, call in enumerate(calls):
+        with pytest.raises(MoEError):
+            call()
+            pytest.fail(f"call {i} was not refused")
