@@ -92,6 +92,47 @@ def test_inverse_root_of_exact_mean_squares(rows, cols):
     assert np.abs(rstd * f64(a)[:, 0] - 1).max() <= 4 * U32
 
 
+@pytest.mark.parametrize("kind", ["layer", "rms"])
+@pytest.mark.parametrize("rows,cols", NORM_KERNELS)
+def test_rows_that_are_not_finite_stay_alone(rows, cols, kind):
+    """An infinity or a NaN in a row makes what IEEE arithmetic makes of the formulas, the same
+    in every kernel, and leaves every other row's bits."""
+    g = gen(rows + 5 * cols)
+    x, dy = randn(g, rows, cols, dtype=torch.float32), randn(g, rows, cols, dtype=torch.float32)
+    w = randn(g, cols, dtype=torch.float32, shift=1.0)
+    b = randn(g, cols, dtype=torch.float32) if kind == "layer" else None
+    inf, nan = float("inf"), float("nan")
+    clean = ops.norm_forward(x, w, b, kind=kind, save=True)
+    for col in (0, cols // 2, cols - 1):
+        for value in (inf, -inf, nan):
+            bad = rows // 2
+            x2 = x.clone()
+            x2[bad, col] = value
+            y, mean, rstd = ops.norm_forward(x2, w, b, kind=kind, save=True)
+            dx, dw, db = ops.norm_backward(dy, x2, w, mean, rstd, kind=kind, bias=b is not None)
+            keep = torch.arange(rows, device="cuda") != bad
+            assert torch.equal(y[keep], clean[0][keep]) and torch.equal(rstd[keep], clean[2][keep])
+            dx0 = ops.norm_backward(dy, x, w, clean[1], clean[2], kind=kind)[0]
+            assert torch.equal(dx[keep], dx0[keep])
+            assert torch.isnan(dx[bad]).all()
+            if kind == "layer":
+                assert torch.equal(mean[keep], clean[1][keep])
+                # x - infinity: no row without a NaN
+                assert torch.equal(mean[bad].cpu(), torch.tensor(value)) or value != value
+                assert value == value or torch.isnan(mean[bad])
+                assert torch.isnan(rstd[bad]) and torch.isnan(y[bad]).all()
+                assert torch.isnan(dw).all() and torch.isfinite(db).all()
+            elif value == value:
+                # the mean square is infinite: 1 / sqrt = 0, 0 for finite elements
+                assert rstd[bad] == 0 and torch.isnan(y[bad, col])
+                others = torch.arange(cols, device="cuda") != col
+                assert (y[bad, others] == 0).all()
+                assert torch.isnan(dw[col]) and torch.isfinite(dw[others]).all()
+            else:
+                assert torch.isnan(rstd[bad]) and torch.isnan(y[bad]).all()
+                assert torch.isnan(dw).all()
+
+
 # ------------------------------------------------------------------------ arguments
 def test_an_argument_without_memory_is_not_an_absent_one():
     x, W1, W3, W2, dout = ffn_case(8, 64, 72, "bf16", 40)
