@@ -384,10 +384,8 @@ PyObject* dropout_add(PyObject*, PyObject* const* a, Py_ssize_t given) {
     const double p = number(a[2], "p");
     const uint64_t* rng = nullptr;
     if (!(p == 0.0 && a[3] == Py_None)) {
-      const bool is_tensor = THPVariable_Check(a[3]);
-      const at::Tensor r = is_tensor ? THPVariable_Unpack(a[3]) : at::Tensor();
-      if (!r.defined() || r.dim() != 1 || r.size(0) != 2 || !r.is_cuda() ||
-          r.get_device() != x.get_device() ||
+      const at::Tensor& r = cuda_tensor(a[3], "rng");
+      if (r.dim() != 1 || r.size(0) != 2 || r.get_device() != x.get_device() ||
           (r.scalar_type() != at::kLong && r.scalar_type() != at::kUInt64) || !r.is_contiguous())
         refuse("rng must be a contiguous int64 (2,) tensor (seed, offset) on " +
                x.device().str());

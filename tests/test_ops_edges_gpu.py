@@ -158,3 +158,16 @@ def test_an_argument_without_memory_is_not_an_absent_one():
         with pytest.raises(MoEError):
             call()
             pytest.fail(f"call {i} was not refused")
+
+
+def test_negated_rng_is_refused():
+    # torch's negative bit: memory holds the unnegated seed and offset
+    x = randn(gen(41), 6, 64)
+    rng = torch.tensor([5, 6], device="cuda")
+    neg = torch._neg_view(rng)
+    with pytest.raises(MoEError):
+        ops.dropout_add_forward(x, x, 0.5, neg)
+    with pytest.raises(MoEError):
+        ops.dropout_add_backward(x, 0.5, neg)
+    want = ops.dropout_add_forward(x, x, 0.5, torch.tensor([-5, -6], device="cuda"))
+    assert torch.equal(ops.dropout_add_forward(x, x, 0.5, neg.resolve_neg()), want)
