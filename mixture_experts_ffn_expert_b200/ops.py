@@ -4,7 +4,8 @@ feed-forward block, dropout with the residual add.
 Each operator has a forward and a backward function over plain tensors
 (``norm_forward`` / ``norm_backward``, ``gated_ffn_forward`` / ``gated_ffn_backward``,
 ``dropout_add_forward`` / ``dropout_add_backward``) and a differentiable function
-(``layer_norm``, ``rms_norm``, ``gated_ffn``, ``dropout_add``) that autograd records.
+(``layer_norm``, ``rms_norm``, ``gated_ffn``, ``dropout_add``) that autograd records. The
+former record nothing: their outputs carry neither a graph nor a forward-mode tangent.
 All arithmetic runs in libmoe_ffn.so on the tensors' device and its current stream;
 outputs and workspaces are torch allocations of the call. Nothing synchronises the host,
 so the calls can be captured into a CUDA graph. (A captured training step should call the
@@ -21,6 +22,7 @@ import os
 from typing import Optional, Tuple
 
 import torch
+from torch.autograd import forward_ad
 
 from .binding import MoEError, _check, load_library
 from .build import host_path
@@ -48,6 +50,19 @@ def _host():
         module.set_error(MoEError)
         _MODULE = module
     return _MODULE
+
+
+def _unrecorded(*arguments) -> bool:
+    """Whether a call may pass its autograd function by and save nothing: grad mode is off and
+    no argument carries a forward-mode tangent. A tangent does not depend on grad mode; the
+    autograd functions have no such derivative and raise, where a plain call would drop it."""
+    if torch.is_grad_enabled():
+        return False
+    # outside every forward-mode level no tensor has a tangent (asking each takes 2 us)
+    if getattr(forward_ad, "_current_level", 0) < 0:
+        return True
+    return not any(isinstance(t, torch.Tensor) and forward_ad.unpack_dual(t).tangent is not None
+                   for t in arguments)
 
 
 # ------------------------------------------------------------------------ norm
@@ -106,7 +121,7 @@ class _Norm(torch.autograd.Function):
 
 
 def _norm(x, weight, bias, eps, kind):
-    if not torch.is_grad_enabled():      # nothing to save (autograd asks the inputs alone)
+    if _unrecorded(x, weight, bias):
         return norm_forward(x, weight, bias, eps, kind)
     return _Norm.apply(x, weight, bias, eps, kind)
 
@@ -163,7 +178,7 @@ class _GatedFFN(torch.autograd.Function):
 
 def gated_ffn(x, W1, W3, W2, activation: str = "silu") -> torch.Tensor:
     """Differentiable gated feed-forward block (see ``gated_ffn_forward``)."""
-    if not torch.is_grad_enabled():
+    if _unrecorded(x, W1, W3, W2):
         return gated_ffn_forward(x, W1, W3, W2, activation)
     return _GatedFFN.apply(x, W1, W3, W2, activation)
 
@@ -207,7 +222,7 @@ class _DropoutAdd(torch.autograd.Function):
 def dropout_add(x, residual, p: float, rng: Optional[torch.Tensor]) -> torch.Tensor:
     """Differentiable residual + dropout(x) (see ``dropout_add_forward``). rng must hold the
     same seed and offset in the backward pass: changing it in place in between raises."""
-    if not torch.is_grad_enabled():
+    if _unrecorded(x, residual):
         return dropout_add_forward(x, residual, p, rng)
     return _DropoutAdd.apply(x, residual, p, rng)
 

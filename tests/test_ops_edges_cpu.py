@@ -45,3 +45,30 @@ def test_tensors_without_memory_are_refused(make):
                  lambda: ops.dropout_add_forward(t, None, 0.0, None)):
         with pytest.raises(MoEError, match="no memory of its own"):
             call()
+
+
+def test_forward_mode_is_refused_with_grad_mode_off(monkeypatch):
+    # the operators have no forward-mode derivative: a tangent may not vanish, whatever the
+    # grad mode (the kernels' part is played by plain torch here)
+    from torch.autograd import forward_ad
+    monkeypatch.setattr(ops, "norm_forward", lambda x, w, b, eps, kind, save=False:
+                        (x * 2, None, x.sum(-1)) if save else x * 2)
+    monkeypatch.setattr(ops, "gated_ffn_forward", lambda x, W1, W3, W2, act, save=False:
+                        (x * 2, x, x) if save else x * 2)
+    monkeypatch.setattr(ops, "dropout_add_forward", lambda x, r, p, rng: x * 2)
+    x, w = torch.ones(4, 8), torch.ones(8)
+    calls = [lambda t: ops.layer_norm(t, w, w), lambda t: ops.rms_norm(t, w),
+             lambda t: ops.layer_norm(x, t[0], w), lambda t: ops.layer_norm(x, w, t[0]),
+             lambda t: ops.gated_ffn(t, x, x, x), lambda t: ops.gated_ffn(x, x, x, t),
+             lambda t: ops.dropout_add(t, x, 0.0, None), lambda t: ops.dropout_add(x, t, 0.0, None),
+             lambda t: ops.gated_ffn_block(t, x, x, x)]
+    for call in calls:
+        for mode in (torch.no_grad, torch.enable_grad):
+            with mode(), forward_ad.dual_level():
+                dual = forward_ad.make_dual(x, torch.ones_like(x))
+                with pytest.raises((RuntimeError, NotImplementedError)):
+                    call(dual)
+        with torch.no_grad(), forward_ad.dual_level():
+            assert torch.equal(call(x), x * 2) or call is calls[-1]
+        with torch.no_grad():
+            assert not call(x).requires_grad

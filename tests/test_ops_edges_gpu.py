@@ -171,3 +171,20 @@ def test_negated_rng_is_refused():
         ops.dropout_add_backward(x, 0.5, neg)
     want = ops.dropout_add_forward(x, x, 0.5, torch.tensor([-5, -6], device="cuda"))
     assert torch.equal(ops.dropout_add_forward(x, x, 0.5, neg.resolve_neg()), want)
+
+
+def test_forward_mode_is_refused_with_grad_mode_off():
+    from torch.autograd import forward_ad
+    x, W1, W3, W2, _ = ffn_case(8, 64, 72, "bf16", 42)
+    rng = torch.tensor([1, 2], device="cuda")
+    want = ops.gated_ffn_block(x, W1, W3, W2, p=0.25, rng=rng)
+    with torch.no_grad(), forward_ad.dual_level():
+        dual = forward_ad.make_dual(x, torch.ones_like(x))
+        dual_w = forward_ad.make_dual(W3, torch.ones_like(W3))
+        for call in (lambda: ops.rms_norm(dual), lambda: ops.layer_norm(dual),
+                     lambda: ops.gated_ffn(dual, W1, W3, W2), lambda: ops.gated_ffn(x, W1, dual_w, W2),
+                     lambda: ops.dropout_add(x, dual, 0.25, rng),
+                     lambda: ops.gated_ffn_block(dual, W1, W3, W2, p=0.25, rng=rng)):
+            with pytest.raises(RuntimeError, match="forward mode|jvp"):
+                call()
+        assert torch.equal(ops.gated_ffn_block(x, W1, W3, W2, p=0.25, rng=rng), want)
