@@ -17,13 +17,26 @@ from .binding import (MOE_OPTION_BIAS_SELECTION_ONLY, MOE_OPTION_CAPACITY_FACTOR
                       MOE_OPTION_INTERLEAVE, MOE_OPTION_SHARED_CONCURRENT,
                       MOE_OPTION_SWIGLU_TILE_COLS, MOE_OPTION_TILE_ROWS, MOE_OPTION_WIDE_TILES,
                       MoEError, Plan)
-from .ops import dropout_add_forward, norm_forward
+from .ops import _has_tangent, dropout_add_forward, norm_forward
 
 __all__ = ["MoELayer", "MoEError"]
 
 
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
+
+
+class _NoBackward(torch.autograd.Function):
+    """The result of a forward-only call on inputs that autograd tracks: asked for a gradient
+    (or a forward-mode tangent) it raises, where a plain result would hold none in silence."""
+
+    @staticmethod
+    def forward(ctx, out, *inputs):
+        return out.view_as(out)
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise MoEError(5, "MoELayer.block has no backward pass; ops.gated_ffn_block has one")
 
 
 class MoELayer:
@@ -153,10 +166,16 @@ class MoELayer:
         ``norm`` is "rms" or "layer"; p = 0 (inference) adds the plain residual, p > 0 draws
         the dropout mask from ``rng`` (see ``ops.dropout_add_forward``). "Shared Expert
         (DeepSeek-V3)", "How it works": the layer's input is normalised, the residual is
-        added at block level.
+        added at block level. Forward only: where x or a norm parameter wants a gradient, the
+        result says so and its backward pass raises ``MoEError``.
         """
         h = norm_forward(x, norm_weight, norm_bias, eps, norm)
-        return dropout_add_forward(self.forward(h), x, p, rng)
+        out = dropout_add_forward(self.forward(h), x, p, rng)
+        inputs = [t for t in (x, norm_weight, norm_bias) if t is not None]
+        if (torch.is_grad_enabled() and any(t.requires_grad for t in inputs)) \
+                or _has_tangent(*inputs):
+            return _NoBackward.apply(out, *inputs)
+        return out
 
     def routing(self) -> Dict[str, torch.Tensor]:
         """idx, w, counts, offsets, perm_src, inv_pos of the last forward (device tensors)."""

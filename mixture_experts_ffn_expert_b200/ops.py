@@ -52,17 +52,20 @@ def _host():
     return _MODULE
 
 
+def _has_tangent(*arguments) -> bool:
+    """Whether an argument carries a forward-mode tangent."""
+    # outside every forward-mode level no tensor does (asking each takes 2 us)
+    if getattr(forward_ad, "_current_level", 0) < 0:
+        return False
+    return any(isinstance(t, torch.Tensor) and forward_ad.unpack_dual(t).tangent is not None
+               for t in arguments)
+
+
 def _unrecorded(*arguments) -> bool:
     """Whether a call may pass its autograd function by and save nothing: grad mode is off and
     no argument carries a forward-mode tangent. A tangent does not depend on grad mode; the
     autograd functions have no such derivative and raise, where a plain call would drop it."""
-    if torch.is_grad_enabled():
-        return False
-    # outside every forward-mode level no tensor has a tangent (asking each takes 2 us)
-    if getattr(forward_ad, "_current_level", 0) < 0:
-        return True
-    return not any(isinstance(t, torch.Tensor) and forward_ad.unpack_dual(t).tangent is not None
-                   for t in arguments)
+    return not torch.is_grad_enabled() and not _has_tangent(*arguments)
 
 
 # ------------------------------------------------------------------------ norm

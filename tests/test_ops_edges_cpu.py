@@ -72,3 +72,30 @@ def test_forward_mode_is_refused_with_grad_mode_off(monkeypatch):
             assert torch.equal(call(x), x * 2) or call is calls[-1]
         with torch.no_grad():
             assert not call(x).requires_grad
+
+
+def test_block_around_the_layer_refuses_gradients(monkeypatch):
+    # forward only: a gradient or a tangent that is wanted may not be lost in silence (plain
+    # torch plays the kernels' part)
+    from torch.autograd import forward_ad
+
+    from mixture_experts_ffn_expert_b200 import layer as layer_mod
+    monkeypatch.setattr(layer_mod, "norm_forward", lambda x, w, b, eps, kind: x * 3)
+    monkeypatch.setattr(layer_mod, "dropout_add_forward", lambda h, x, p, rng: h.detach() + x)
+    layer = layer_mod.MoELayer.__new__(layer_mod.MoELayer)
+    layer.forward = lambda h: h
+    x, w = torch.ones(4, 8), torch.ones(8)
+    out = layer.block(x, w)
+    assert not out.requires_grad and torch.equal(out, x * 4)
+    for wants in (0, 1):
+        args = [x.clone(), w.clone()]
+        args[wants].requires_grad_(True)
+        out = layer.block(*args, p=0.1)
+        assert out.requires_grad and torch.equal(out, x * 4)
+        with pytest.raises(MoEError, match="no backward pass"):
+            out.sum().backward()
+        with torch.no_grad():
+            assert not layer.block(*args).requires_grad
+    for mode in (torch.no_grad, torch.enable_grad):
+        with mode(), forward_ad.dual_level(), pytest.raises(RuntimeError):
+            layer.block(forward_ad.make_dual(x, torch.ones_like(x)), w)

@@ -188,3 +188,23 @@ def test_forward_mode_is_refused_with_grad_mode_off():
             with pytest.raises(RuntimeError, match="forward mode|jvp"):
                 call()
         assert torch.equal(ops.gated_ffn_block(x, W1, W3, W2, p=0.25, rng=rng), want)
+
+
+def test_block_around_the_layer_refuses_gradients():
+    from mixture_experts_ffn_expert_b200.inputs import WORKLOADS, make_layer_inputs
+    from mixture_experts_ffn_expert_b200.layer import MoELayer
+    s = WORKLOADS["tiny_t256_d128_f64_e31k7_s1"]
+    inp = make_layer_inputs(s, seed=0, device="cuda")
+    layer = MoELayer(s.d, s.f, s.n_routed, s.top_k, s.n_shared, s.renorm, inp, bias=inp["bias"])
+    w = randn(gen(43), s.d, scale=0.1, shift=1.0)
+    rng = torch.tensor([1, 2], device="cuda")
+    want = layer.block(inp["x"], w, p=0.1, rng=rng)
+    assert not want.requires_grad
+    for x, v in ((inp["x"].clone().requires_grad_(True), w),
+                 (inp["x"], w.clone().requires_grad_(True))):
+        out = layer.block(x, v, p=0.1, rng=rng)
+        assert torch.equal(out, want)
+        with pytest.raises(MoEError, match="no backward pass"):
+            out.sum().backward()
+        with torch.no_grad():
+            assert not layer.block(x, v, p=0.1, rng=rng).requires_grad
