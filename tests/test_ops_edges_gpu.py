@@ -6,10 +6,11 @@ import pytest
 import torch
 
 from mixture_experts_ffn_expert_b200 import ops
-from mixture_experts_ffn_expert_b200.binding import MoEError
+from mixture_experts_ffn_expert_b200.binding import MoEError, load_library
 from oracle import ops_oracle as O
 from test_ops_edges_cpu import Wrapper
-from test_ops_gpu import DT, K, U32, close, f64, ffn_case, gen, randn
+from test_ops_gpu import (DT, K, U32, close, drop_tol, f64, ffn_bounds, ffn_case, gen,
+                          norm_bounds, randn, unit)
 
 pytestmark = pytest.mark.gpu
 
@@ -208,3 +209,133 @@ def test_block_around_the_layer_refuses_gradients():
             out.sum().backward()
         with torch.no_grad():
             assert not layer.block(x, v, p=0.1, rng=rng).requires_grad
+
+
+# ------------------------------------------------------------------------ C interface
+def stream():
+    return torch.cuda.current_stream().cuda_stream
+
+
+def padded(rows, cols, pad, dtype):
+    """An output whose rows are cols + pad apart, filled with a sentinel, and its view."""
+    buf = torch.full((rows, cols + pad), 7.0, dtype=dtype, device="cuda")
+    return buf, buf[:, :cols]
+
+
+def padding_kept(buf, cols):
+    return torch.equal(buf[:, cols:], torch.full_like(buf[:, cols:], 7.0))
+
+
+@pytest.mark.parametrize("pad", [8, 5])
+@pytest.mark.parametrize("rows,cols", NORM_KERNELS)
+def test_norm_padded_outputs(rows, cols, pad):
+    lib = load_library()
+    g = gen(rows + 9 * cols)
+    x, dy = randn(g, rows, cols), randn(g, rows, cols)
+    w, b = randn(g, cols, shift=1.0), randn(g, cols)
+    y, mean, rstd = ops.norm_forward(x, w, b, save=True)
+    buf, view = padded(rows, cols, pad, x.dtype)
+    assert lib.moe_norm_forward(0, 0, 0, rows, cols, x.data_ptr(), cols, w.data_ptr(),
+                                b.data_ptr(), 1e-5, buf.data_ptr(), cols + pad, None, None,
+                                stream()) == 0
+    want = norm_bounds(f64(x), f64(w), f64(b), f64(dy), x.dtype, x.dtype, "layer", 1e-5)
+    close(view, *want[0], "y")
+    assert padding_kept(buf, cols)
+    buf, view = padded(rows, cols, pad, x.dtype)
+    dw2, db2 = torch.empty_like(w), torch.empty_like(b)
+    ws = torch.empty(lib.moe_norm_workspace_bytes(0, rows, cols), dtype=torch.uint8, device="cuda")
+    assert lib.moe_norm_backward(0, 0, 0, rows, cols, dy.data_ptr(), cols, x.data_ptr(), cols,
+                                 w.data_ptr(), mean.data_ptr(), rstd.data_ptr(), buf.data_ptr(),
+                                 cols + pad, dw2.data_ptr(), db2.data_ptr(), ws.data_ptr(),
+                                 ws.numel(), stream()) == 0
+    for name, got, (ref, tol) in zip(("dx", "dweight", "dbias"), (view, dw2, db2), want[1:]):
+        close(got, ref, tol, name)
+    assert padding_kept(buf, cols)
+
+
+# streamed, single CTAs, split reductions beyond a token tile, pairs
+FFN_KERNELS = [(1, 136, 264), (40, 136, 264), (100, 520, 520), (128, 1024, 1024), (300, 136, 264),
+               (333, 2048, 1408), (2321, 2088, 2632)]
+
+
+@pytest.mark.parametrize("T,d,f", FFN_KERNELS)
+def test_gated_ffn_padded_tensors(T, d, f):
+    lib = load_library()
+    x, W1, W3, W2, dout = ffn_case(T, d, f, "bf16", 44)
+    out, gate, up = ops.gated_ffn_forward(x, W1, W3, W2, save=True)
+    grads = ops.gated_ffn_backward(dout, x, W1, W3, W2, gate, up)
+    ld = d + 24
+    wide = lambda t: torch.cat([t, torch.full((T, 24), float("nan"), device="cuda",  # noqa: E731
+                                              dtype=t.dtype)], 1)
+    xw, dw = wide(x), wide(dout)
+    ws = torch.empty(lib.moe_gated_ffn_workspace_bytes(T, d, f, 1), dtype=torch.uint8,
+                     device="cuda")
+    buf, view = padded(T, d, 24, x.dtype)
+    P = lambda *ts: [t.data_ptr() for t in ts]                             # noqa: E731
+    assert lib.moe_gated_ffn_forward(0, 0, T, d, f, xw.data_ptr(), ld, *P(W1, W3, W2, buf), ld,
+                                     None, None, ws.data_ptr(), ws.numel(), stream()) == 0
+    assert torch.equal(view, out) and padding_kept(buf, d)
+    buf, view = padded(T, d, 24, x.dtype)
+    mine = [torch.empty_like(t) for t in grads[1:]]
+    assert lib.moe_gated_ffn_backward(0, 0, T, d, f, dw.data_ptr(), ld, xw.data_ptr(), ld,
+                                      *P(W1, W3, W2, gate, up, buf), ld, *P(*mine), ws.data_ptr(),
+                                      ws.numel(), stream()) == 0
+    assert torch.equal(view, grads[0]) and padding_kept(buf, d)
+    assert all(torch.equal(a, b) for a, b in zip(mine, grads[1:]))
+    # dx alone: its own launch of another kernel for few tokens
+    buf, view = padded(T, d, 24, x.dtype)
+    assert lib.moe_gated_ffn_backward(0, 0, T, d, f, dw.data_ptr(), ld, xw.data_ptr(), ld,
+                                      *P(W1, W3, W2, gate, up, buf), ld, None, None, None,
+                                      ws.data_ptr(), ws.numel(), stream()) == 0
+    alone = ops.gated_ffn_backward(dout, x, W1, W3, W2, gate, up,
+                                   needs=(True, False, False, False))[0]
+    assert torch.equal(view, alone) and padding_kept(buf, d)
+    want, tol = ffn_bounds(*(f64(t) for t in (x, W1, W3, W2, dout)), "silu", x.dtype)["dx"]
+    close(alone, want, tol, "dx alone")
+    ops.device_status()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("rows,cols", [(1, 1), (3, 7), (33, 128), (777, 1001)])
+def test_dropout_c_interface(rows, cols, dtype):
+    lib = load_library()
+    g = gen(rows + 11 * cols)
+    dt = DT[dtype]
+    code = {"bf16": 0, "fp32": 2}[dtype]
+    x, res = randn(g, rows, cols, dtype=dt), randn(g, rows, cols, dtype=dt)
+    rng = torch.tensor([31, 32], device="cuda")
+    p = 0.3
+    out = ops.dropout_add_forward(x, res, p, rng)
+    want = O.dropout_add(f64(x), None, p, 31, 32)
+    dx = torch.empty_like(x)
+    assert lib.moe_dropout_backward(code, rows, cols, x.data_ptr(), cols, p, rng.data_ptr(),
+                                    dx.data_ptr(), cols, stream()) == 0
+    close(dx, want, drop_tol(f64(x), None, p, dt, want), "dx")
+    # in place: over dout, over x, over the residual
+    for over in ("dout", "x", "residual"):
+        a, r = x.clone(), res.clone()
+        target = r if over == "residual" else a
+        if over == "dout":
+            assert lib.moe_dropout_backward(code, rows, cols, a.data_ptr(), cols, p,
+                                            rng.data_ptr(), a.data_ptr(), cols, stream()) == 0
+            assert torch.equal(a, dx)
+            continue
+        assert lib.moe_dropout_forward(code, rows, cols, a.data_ptr(), cols, r.data_ptr(), cols, p,
+                                       rng.data_ptr(), target.data_ptr(), cols, stream()) == 0
+        assert torch.equal(target, out) and torch.equal(r if over == "x" else a,
+                                                        res if over == "x" else x)
+    # padded outputs, and in place with padding (strided kernels)
+    for pad in (8, 5):
+        buf, view = padded(rows, cols, pad, dt)
+        assert lib.moe_dropout_forward(code, rows, cols, x.data_ptr(), cols, res.data_ptr(), cols, p,
+                                       rng.data_ptr(), buf.data_ptr(), cols + pad, stream()) == 0
+        assert torch.equal(view, out) and padding_kept(buf, cols)
+        view.copy_(x)
+        assert lib.moe_dropout_forward(code, rows, cols, buf.data_ptr(), cols + pad,
+                                       res.data_ptr(), cols, p, rng.data_ptr(), buf.data_ptr(),
+                                       cols + pad, stream()) == 0
+        assert torch.equal(view, out) and padding_kept(buf, cols)
+        buf, view = padded(rows, cols, pad, dt)
+        assert lib.moe_dropout_backward(code, rows, cols, x.data_ptr(), cols, p, rng.data_ptr(),
+                                        buf.data_ptr(), cols + pad, stream()) == 0
+        assert torch.equal(view, dx) and padding_kept(buf, cols)
