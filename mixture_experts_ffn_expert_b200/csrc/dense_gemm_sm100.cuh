@@ -341,15 +341,16 @@ __global__ void __launch_bounds__(kDgThreads, 1)
           }
         }
       }
-      if (!ok) {
-        raise_abort(s_abort, P.status);
-        if (leader)                 // copies in flight get a bounded time to land
-          for (int i = 0; i < kS; ++i)
-            if (issued_mask & (1u << i)) {
-              int never = 0;
-              mbar_wait(smem_u32(&full_bar[i]), (issued_par >> i) & 1u, &never);
-            }
-      }
+      if (!ok) raise_abort(s_abort, P.status);
+      // The block keeps its shared memory until its copies have landed, given up or not (also by
+      // another role, after this one issued its last): a bounded time. The leader's barriers
+      // count both CTAs' copies.
+      if (leader)
+        for (int i = 0; i < kS; ++i)
+          if (issued_mask & (1u << i)) {
+            int never = 0;
+            mbar_wait(smem_u32(&full_bar[i]), (issued_par >> i) & 1u, &never);
+          }
     }
     __syncwarp();
   } else if (warp == 1) {

@@ -164,14 +164,14 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
           ph ^= 1u;
         }
       }
-      if (!ok) {
-        raise_abort(s_abort, P.status);
-        for (int i = 0; i < kS; ++i)      // copies in flight get a bounded time to land
-          if (issued_mask & (1u << i)) {
-            int never = 0;
-            mbar_wait(smem_u32(&full_bar[i]), (issued_par >> i) & 1u, &never);
-          }
-      }
+      if (!ok) raise_abort(s_abort, P.status);
+      // The block keeps its shared memory until its copies have landed, given up or not (also by
+      // the MMA issuer, after this role issued its last): a bounded time.
+      for (int i = 0; i < kS; ++i)
+        if (issued_mask & (1u << i)) {
+          int never = 0;
+          mbar_wait(smem_u32(&full_bar[i]), (issued_par >> i) & 1u, &never);
+        }
     }
     __syncwarp();
     if (weights && P.early) pdl_wait();
