@@ -136,6 +136,9 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
       uint32_t ph = 0, issued_mask = 0, issued_par = 0;
       bool ok = true;
       for (int kb = kb_lo; kb < kb_hi; ++kb) {
+        // the ring is full: its first stage is free only when the tokens have come, and the
+        // bounded wait for that must not begin while the predecessor runs
+        if (weights && P.early && kb == kb_lo + kS) pdl_wait();
         ok = mbar_wait(smem_u32(&empty_bar[s]), ph ^ 1u, s_abort);
         if (!ok) break;
         const int seg = kb >= P.kb[0];
@@ -165,6 +168,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
         }
       }
       if (!ok) raise_abort(s_abort, P.status);
+      if (weights && P.early) pdl_wait();       // the stages fill only with the tokens
       // The block keeps its shared memory until its copies have landed, given up or not (also by
       // the MMA issuer, after this role issued its last): a bounded time.
       for (int i = 0; i < kS; ++i)
@@ -206,8 +210,9 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
     }
     __syncwarp();
   }
-  // Dependents may start only now: every thread is past its wait, so what came before this
-  // kernel is complete and a dependent may read the weights early.
+  // Dependents may start only now. The trigger fires with a block's first thread here, and any
+  // thread that has passed its wait proves that what came before this kernel is complete, so a
+  // dependent may read the weights early. (Warp 0 of an early launch may be before its wait.)
   pdl_launch_dependents();
 
   // ------------------------------------------------------------ partial rows to their owners
