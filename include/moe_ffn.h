@@ -390,6 +390,14 @@ int moe_dropout_backward(int dtype, int64_t rows, int64_t cols, const void* dout
  * wait since the last read (its outputs are invalid). */
 int moe_ops_device_status(void);
 
+/* Test hook for the failure path, not for normal use. Arms the launch-th (1, 2, ...) of the
+ * calling host thread's next launches of a kernel of the operators that waits for bulk copies
+ * (the products, and the norms over many rows): one block of it withholds its first copy, the
+ * waits for that copy run out (2 s), and the kernel sets the status word, lets its own copies
+ * land, frees its tensor memory and returns. That call's outputs are invalid; the context
+ * stays usable. 0 disarms. No fault, trap or unbounded wait. */
+int moe_ops_test_wait_timeout(int launch);
+
 #ifdef __cplusplus
 }
 #endif

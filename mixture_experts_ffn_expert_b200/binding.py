@@ -24,6 +24,7 @@ EXPORTED_SYMBOLS = [
     "moe_norm_forward", "moe_norm_workspace_bytes", "moe_norm_backward",
     "moe_gated_ffn_workspace_bytes", "moe_gated_ffn_forward", "moe_gated_ffn_backward",
     "moe_dropout_forward", "moe_dropout_backward", "moe_ops_device_status",
+    "moe_ops_test_wait_timeout",
 ]
 MOE_OPTION_PAIR_MIN_ROWS = 1
 MOE_OPTION_WIDE_TILES = 2
@@ -106,6 +107,7 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
                                      _vp]),
         "moe_dropout_backward": (_i, [_i, _i64, _i64, _vp, _i64, _dbl, _vp, _vp, _i64, _vp]),
         "moe_ops_device_status": (_i, []),
+        "moe_ops_test_wait_timeout": (_i, [_i]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)

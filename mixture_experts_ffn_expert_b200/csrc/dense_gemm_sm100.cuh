@@ -75,6 +75,7 @@ struct DenseParams {
   const void *gate, *up;            // dh: the saved pre-activations (M, N)
   int save;                         // gate/up: store them
   int act;
+  int test_withhold;                // test hook: worker 0 withholds its first stage's copy of A
   int* status;
 };
 
@@ -291,7 +292,7 @@ __global__ void __launch_bounds__(kDgThreads, 1)
       const bool is_a = warp == 0;
       int s = 0;
       uint32_t ph = 0, issued_mask = 0, issued_par = 0;
-      bool ok = true;
+      bool ok = true, withhold = P.test_withhold && worker == 0 && leader && is_a;
       for (int it = 0; ok; ++it) {
         const int tile = tile_of(P, worker, workers, it);
         if (tile >= P.total_tiles) break;
@@ -310,6 +311,11 @@ __global__ void __launch_bounds__(kDgThreads, 1)
           for (int kb = 0; kb < nkb; ++kb) {
             ok = mbar_wait(smem_u32(&empty_bar[s]), ph ^ 1u, s_abort);
             if (!ok) break;
+            if (withhold) {           // the stage's barrier never completes: all roles give up
+              withhold = false;
+              s = 1;
+              continue;
+            }
             uint32_t fb = smem_u32(&full_bar[s]);
             if (is_a && leader) mbar_arrive_expect_tx(fb, (PAIR ? 2 : 1) * kDgStageBytes);
             if (PAIR) fb = mapa_shared(fb, 0);

@@ -22,6 +22,9 @@ using moe::set_error;
 // Set by a kernel that gave up a bounded wait; one word a device.
 __device__ int g_ops_status;
 
+// Launches of this host thread until the one whose first copy is withheld (0: none).
+thread_local int t_test_timeout = 0;
+
 constexpr int kMaxDevices = 64;
 
 struct DeviceInfo {
@@ -181,6 +184,7 @@ cudaError_t launch(GemmLaunch& L, const DeviceInfo& d, cudaStream_t st) {
     if (late < workers) L.P.extra = extra;
   }
   L.P.status = d.status;
+  L.P.test_withhold = moe::take_test_timeout();
   L.P.n_maps = L.n_maps;
   return launch_overlapped(moe::dense_gemm_kernel<T, EPI, PAIR>,
                            dim3(PAIR ? 2 * workers : workers), dim3(moe::kDgThreads),
@@ -271,6 +275,7 @@ cudaError_t launch_stream_columns(StreamLaunch& L, const DeviceInfo& d, cudaStre
   const int64_t tiles = L.P.t_tiles * ceil_div(L.P.N, EPI == moe::kGemmGluForward ? 64 : 128);
   const int ranks = stream_ranks(tiles, L.P.kb[0] + L.P.kb[1], d.sms);
   L.P.status = d.status;
+  L.P.test_withhold = moe::take_test_timeout();
   return launch_overlapped(moe::stream_gemm_kernel<T, EPI, NB>, dim3(unsigned(tiles * ranks)),
                            dim3(moe::kStreamThreads), moe::StreamCfg<NB>::kSmem, st, ranks, L.maps,
                            L.P);
@@ -329,6 +334,11 @@ int ops_device(OpsDevice* out) {
   out->sms = d->sms;
   out->status = d->status;
   return MOE_OK;
+}
+
+int take_test_timeout() {
+  if (t_test_timeout == 0) return 0;
+  return --t_test_timeout == 0;
 }
 }  // namespace moe
 
@@ -549,6 +559,12 @@ int moe_gated_ffn_backward(int act, int dtype, int64_t T, int64_t d, int64_t f, 
   if (!L.ok) return set_error(MOE_CUDA_ERROR, "tensor map encoding failed");
   e = launch_any<moe::kGemmPlain>(L, pair, *dev, st);
   if (e != cudaSuccess) return cuda_error(e, "gated feed-forward gradient launch");
+  return MOE_OK;
+}
+
+int moe_ops_test_wait_timeout(int launch) {
+  if (launch < 0) return set_error(MOE_INVALID_ARG, "launch must be >= 0");
+  t_test_timeout = launch;
   return MOE_OK;
 }
 

@@ -414,6 +414,7 @@ struct NormTile {
   int contiguous;          // rows follow one another: one copy a tile
   uint32_t slot_bytes;     // of one matrix
   uint32_t weight_bytes;   // backward: the weight staged in front of the ring
+  int test_withhold;       // test hook: block 0 withholds its first tile's copies
 };
 
 struct TileShared {
@@ -612,6 +613,10 @@ __device__ __forceinline__ void tile_producer(const NormParams& P, const NormTil
   for (int t = 0; t < tiles; ++t) {
     tile_wait(&sh.free[s], ph ^ 1u, &sh.abort, status);
     if (*static_cast<volatile int*>(&sh.abort)) break;
+    if (t == 0 && L.test_withhold && blockIdx.x == 0) {     // slot 0 never fills: all roles give up
+      s = 1;
+      continue;
+    }
     const long long row = lo + static_cast<long long>(t) * L.rows;
     const int n = static_cast<int>(hi - row < L.rows ? hi - row : L.rows);
     uint8_t* slot = ring + static_cast<size_t>(s) * PLANES * L.slot_bytes;

@@ -85,6 +85,7 @@ bool tile_shape(moe::NormTile* L, const moe::NormParams& P, int vec, int vpt, in
   L->group = round32((n + vpt - 1) / vpt);
   if (L->group > column_warps * 32) return false;
   L->contiguous = contiguous;
+  L->test_withhold = 0;
   L->weight_bytes = planes == 2 ? uint32_t((size_t(P.cols) * 4 + 127) / 128 * 128) : 0;
   if (L->weight_bytes >= kTileSmem) return false;
   const size_t room = kTileSmem - L->weight_bytes;
@@ -118,12 +119,13 @@ cudaError_t tile_attribute(K kernel, std::atomic<uint64_t>* done, int device) {
 }
 
 template <typename T, int VEC, int VPT, bool RMS>
-cudaError_t launch_norm_forward_tile(const moe::NormParams& P, const moe::NormTile& L, size_t smem,
+cudaError_t launch_norm_forward_tile(const moe::NormParams& P, moe::NormTile L, size_t smem,
                                      const moe::OpsDevice& d, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
   const auto kernel = moe::norm_forward_tile_kernel<T, VEC, VPT, kColumnWarps, RMS>;
   const cudaError_t e = tile_attribute(kernel, &done, d.index);
   if (e != cudaSuccess) return e;
+  L.test_withhold = moe::take_test_timeout();
   const int64_t blocks = P.rows < d.sms ? P.rows : d.sms;
   return launch_overlapped(kernel, dim3(unsigned(blocks)),
                            dim3(moe::tile_threads(kColumnWarps)), smem, st, 1, P, L, d.status);
@@ -194,12 +196,13 @@ cudaError_t launch_norm_backward(const moe::NormParams& P, int group, int* block
 }
 
 template <typename T, int VEC, int VPT, bool RMS, bool GRADW>
-cudaError_t launch_norm_backward_tile(const moe::NormParams& P, const moe::NormTile& L, size_t smem,
+cudaError_t launch_norm_backward_tile(const moe::NormParams& P, moe::NormTile L, size_t smem,
                                       const moe::OpsDevice& d, int* blocks, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
   const auto kernel = moe::norm_backward_tile_kernel<T, VEC, VPT, kColumnWarps, RMS, GRADW>;
   const cudaError_t e = tile_attribute(kernel, &done, d.index);
   if (e != cudaSuccess) return e;
+  L.test_withhold = moe::take_test_timeout();
   // no more blocks than partial rows in the workspace: min(rows, kNormBlocks)
   *blocks = d.sms < kNormBlocks ? d.sms : kNormBlocks;
   if (P.rows < *blocks) *blocks = static_cast<int>(P.rows);

@@ -26,6 +26,10 @@ struct OpsDevice {
 };
 int ops_device(OpsDevice* out);
 
+// Test hook (moe_ops_test_wait_timeout): whether the launch being put together on this host
+// thread is the armed one; counts the launch.
+int take_test_timeout();
+
 // Launch with programmatic stream serialisation, optionally as clusters of `cluster` CTAs:
 // the kernel may start its prologue while its predecessor in the stream finishes, and
 // waits (griddepcontrol.wait) before it touches global memory.

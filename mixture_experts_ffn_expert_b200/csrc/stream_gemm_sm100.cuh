@@ -53,6 +53,7 @@ struct StreamParams {
   void* out;                // plain: (T, N), rows ldo apart
   long long ldo;
   void *gate, *up, *hidden, *dgate, *dup;
+  int test_withhold;        // test hook: block 0 withholds its first stage's weights
   int* status;
 };
 
@@ -134,13 +135,18 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
     if (elect_one()) {
       int s = 0;
       uint32_t ph = 0, issued_mask = 0, issued_par = 0;
-      bool ok = true;
+      bool ok = true, withhold = P.test_withhold && weights && blockIdx.x == 0;
       for (int kb = kb_lo; kb < kb_hi; ++kb) {
         // the ring is full: its first stage is free only when the tokens have come, and the
         // bounded wait for that must not begin while the predecessor runs
         if (weights && P.early && kb == kb_lo + kS) pdl_wait();
         ok = mbar_wait(smem_u32(&empty_bar[s]), ph ^ 1u, s_abort);
         if (!ok) break;
+        if (withhold) {               // the stage's barrier never completes: all roles give up
+          withhold = false;
+          s = 1;
+          continue;
+        }
         const int seg = kb >= P.kb[0];
         const int k0 = (seg ? kb - P.kb[0] : kb) * 64;
         const uint32_t fb = smem_u32(&full_bar[s]);

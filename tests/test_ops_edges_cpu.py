@@ -99,3 +99,10 @@ def test_block_around_the_layer_refuses_gradients(monkeypatch):
     for mode in (torch.no_grad, torch.enable_grad):
         with mode(), forward_ad.dual_level(), pytest.raises(RuntimeError):
             layer.block(forward_ad.make_dual(x, torch.ones_like(x)), w)
+
+
+def test_wait_timeout_hook_refuses_negative_launches():
+    from mixture_experts_ffn_expert_b200.binding import load_library
+    lib = load_library()
+    assert lib.moe_ops_test_wait_timeout(-1) == 2
+    assert lib.moe_ops_test_wait_timeout(0) == 0

@@ -339,3 +339,62 @@ def test_dropout_c_interface(rows, cols, dtype):
         assert lib.moe_dropout_backward(code, rows, cols, x.data_ptr(), cols, p, rng.data_ptr(),
                                         buf.data_ptr(), cols + pad, stream()) == 0
         assert torch.equal(view, dx) and padding_kept(buf, cols)
+
+
+# ------------------------------------------------------------------------ failure path
+def norm_call(rows, cols, backward):
+    g = gen(rows + cols)
+    x, dy = randn(g, rows, cols), randn(g, rows, cols)
+    w = randn(g, cols, shift=1.0)
+    _, mean, rstd = ops.norm_forward(x, w, save=True)
+    if backward:
+        return lambda: ops.norm_backward(dy, x, w, mean, rstd)[:2]
+    return lambda: (ops.norm_forward(x, w),)
+
+
+def ffn_call(T, d, f, needs=None):
+    x, W1, W3, W2, dout = ffn_case(T, d, f, "bf16", 45)
+    _, gate, up = ops.gated_ffn_forward(x, W1, W3, W2, save=True)
+    if needs:
+        return lambda: [t for t in ops.gated_ffn_backward(dout, x, W1, W3, W2, gate, up,
+                                                          needs=needs) if t is not None]
+    return lambda: (ops.gated_ffn_forward(x, W1, W3, W2),)
+
+
+ALL, DX = (True,) * 4, (True, False, False, False)
+
+
+@pytest.mark.parametrize("make,launch", [
+    (lambda: norm_call(700, 1000, False), 1), (lambda: norm_call(700, 1003, False), 1),
+    (lambda: norm_call(700, 1000, True), 1), (lambda: norm_call(3000, 128, True), 1),
+    (lambda: ffn_call(1, 136, 2048), 1), (lambda: ffn_call(24, 2048, 1408), 2),
+    (lambda: ffn_call(100, 2048, 2816), 1), (lambda: ffn_call(40, 2048, 1408, DX), 2),
+    (lambda: ffn_call(128, 1024, 1024), 1), (lambda: ffn_call(128, 1024, 1024), 2),
+    (lambda: ffn_call(300, 136, 264, ALL), 2),
+    (lambda: ffn_call(2321, 2088, 2632), 1), (lambda: ffn_call(2321, 2088, 2632, ALL), 1),
+    (lambda: ffn_call(2321, 2088, 2632, ALL), 2),
+], ids=["norm", "norm_odd", "norm_backward", "norm_backward_short", "stream", "stream_early",
+        "stream_128", "stream_dx_early", "single", "single_down", "single_gradients", "pairs",
+        "pairs_dh", "pairs_gradients"])
+def test_a_wait_that_runs_out_is_reported_and_the_context_recovers(make, launch):
+    """The failure path without a fault: one block withholds its first copy, the bounded waits
+    for it run out (2 s), the kernel reports and returns; the next call has its usual bits."""
+    import time
+    lib = load_library()
+    call = make()
+    want = [t.clone() for t in call()]
+    ops.device_status()
+    assert lib.moe_ops_test_wait_timeout(launch) == 0
+    torch.cuda.synchronize()
+    t0 = time.perf_counter()
+    call()
+    torch.cuda.synchronize()
+    waited = time.perf_counter() - t0
+    assert lib.moe_ops_test_wait_timeout(0) == 0
+    with pytest.raises(MoEError) as e:
+        ops.device_status()
+    assert e.value.status == 6                     # MOE_DEVICE_TIMEOUT
+    ops.device_status()                            # reading cleared it
+    assert 1.5 < waited < 30.0, waited             # bounded waits, not a hang
+    assert all(torch.equal(a, b) for a, b in zip(call(), want))
+    ops.device_status()
