@@ -6,6 +6,8 @@ binding that loads them. nvcc cross-compiles, so no GPU is needed to build.
 """
 from __future__ import annotations
 
+import importlib.metadata
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -23,6 +25,7 @@ HEADERS = ["ptx_sm100.cuh", "gemm_sm100.cuh", "route.cuh", "router_sm100.cuh",
 
 HOST_NAME = "_moe_host.so"
 HOST_SOURCE = "host_ops.cpp"
+STAMP_SUFFIX = ".built-with"      # beside the module: the torch and Python it was compiled against
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -59,16 +62,47 @@ def _stale(target: str, sources) -> bool:
 
 def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
     """Compile the CUDA library and the module behind ops.py (each skipped when it is newer
-    than its sources). Returns the CUDA library's path."""
+    than its sources). Returns the CUDA library's path. The C ABI needs the library alone: where
+    torch or a C++ compiler is absent, the module is left out with a message (and ops.py, which
+    needs it, raises when it is called)."""
     target = _build_library(force, verbose, extra_flags)
     _build_host(force, verbose)
     return target
 
 
+def _torch_tag() -> str:
+    """The torch and Python that a module is compiled against ("" without torch)."""
+    if importlib.util.find_spec("torch") is None:
+        return ""
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        import torch
+        version = torch.__version__
+    return f"torch {version}, {sys.implementation.cache_tag}"
+
+
+def _host_stale(target: str, tag: str) -> bool:
+    if _stale(target, [HOST_SOURCE]):
+        return True
+    try:
+        with open(target + STAMP_SUFFIX) as f:
+            return f.read() != tag
+    except OSError:
+        return True
+
+
 def _build_host(force: bool, verbose: bool) -> None:
     """The torch-facing module: plain C++ against torch's headers, linked to the library."""
     target = host_path()
-    if not force and not _stale(target, [HOST_SOURCE]):
+    tag = _torch_tag()
+    compiler = os.environ.get("CXX", "g++")
+    missing = "torch" if not tag else compiler if shutil.which(compiler) is None else None
+    if missing:
+        print(f"{HOST_NAME} is not built: {missing} was not found (the torch functions of "
+              "ops.py need it, the C ABI does not)", file=sys.stderr)
+        return
+    if not force and not _host_stale(target, tag):
         return
     import sysconfig
 
@@ -79,7 +113,7 @@ def _build_host(force: bool, verbose: bool) -> None:
     cuda_include = os.path.join(os.path.dirname(os.path.dirname(nvcc_path())), "include")
     includes = [INCLUDE, *cpp_extension.include_paths(), sysconfig.get_paths()["include"],
                 cuda_include]
-    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+    cmd = [compiler, "-O2", "-std=c++17", "-fPIC", "-shared",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            *[f"-I{i}" for i in includes], os.path.join(CSRC, HOST_SOURCE), "-o", tmp,
            f"-L{LIBDIR}", f"-l:{LIBNAME}", "-Wl,-rpath,$ORIGIN", f"-L{torch_lib}",
@@ -90,6 +124,8 @@ def _build_host(force: bool, verbose: bool) -> None:
     if res.returncode != 0:
         raise RuntimeError(f"{cmd[0]} failed ({res.returncode}):\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, target)
+    with open(target + STAMP_SUFFIX, "w") as f:
+        f.write(tag)
 
 
 def _build_library(force: bool, verbose: bool, extra_flags) -> str:

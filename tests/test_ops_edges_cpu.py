@@ -106,3 +106,26 @@ def test_wait_timeout_hook_refuses_negative_launches():
     lib = load_library()
     assert lib.moe_ops_test_wait_timeout(-1) == 2
     assert lib.moe_ops_test_wait_timeout(0) == 0
+
+
+def test_the_c_library_builds_without_torch_or_a_compiler(monkeypatch, capsys):
+    # the C ABI does not need the torch module; ops.py without it raises (tested elsewhere)
+    def no_compiler_runs(*a, **k):
+        raise AssertionError("nothing may be compiled here")
+    monkeypatch.setattr(build_mod.subprocess, "run", no_compiler_runs)
+    real = build_mod.importlib.util.find_spec
+    monkeypatch.setattr(build_mod.importlib.util, "find_spec",
+                        lambda name, *a: None if name == "torch" else real(name, *a))
+    assert build_mod.build() == build_mod.lib_path()
+    assert "torch was not found" in capsys.readouterr().err
+    monkeypatch.undo()
+    monkeypatch.setenv("CXX", "no-such-compiler")
+    assert build_mod.build() == build_mod.lib_path()
+    assert "no-such-compiler was not found" in capsys.readouterr().err
+
+
+def test_the_module_is_stale_when_torch_changes(monkeypatch):
+    tag = build_mod._torch_tag()
+    assert torch.__version__ in tag
+    assert not build_mod._host_stale(build_mod.host_path(), tag)
+    assert build_mod._host_stale(build_mod.host_path(), tag + "x")
