@@ -170,13 +170,18 @@ __device__ __forceinline__ float act_value(float a, int act) {
   const float z = act == kActSilu ? a : 1.5957691216057308f * (a + 0.044715f * a * a * a);
   return a * __fdividef(1.0f, 1.0f + __expf(-z));
 }
+// The gate is a saved one, infinite where it passed the 16-bit type's range; below -1e12 it is
+// taken as -1e12, and for the derivative above 1e12 as 1e12 (s is exactly 0 or 1 long before), so
+// that 0 times infinity does not make a NaN of a gradient that is 0 or 1.
 __device__ __forceinline__ void act_value_grad(float a, int act, float& v, float& d) {
-  const float a2 = a * a;
-  const float z = act == kActSilu ? a : 1.5957691216057308f * (a + 0.044715f * a * a2);
-  const float dz = act == kActSilu ? 1.0f : 1.5957691216057308f * (1.0f + 0.134145f * a2);
+  a = a < -1e12f ? -1e12f : a;
+  const float b = a > 1e12f ? 1e12f : a;
+  const float b2 = b * b;
+  const float z = act == kActSilu ? b : 1.5957691216057308f * (b + 0.044715f * b * b2);
+  const float dz = act == kActSilu ? 1.0f : 1.5957691216057308f * (1.0f + 0.134145f * b2);
   const float s = __fdividef(1.0f, 1.0f + __expf(-z));
   v = a * s;
-  d = s + v * (1.0f - s) * dz;
+  d = s + b * s * (1.0f - s) * dz;
 }
 
 template <typename T>

@@ -398,3 +398,41 @@ def test_a_wait_that_runs_out_is_reported_and_the_context_recovers(make, launch)
     assert 1.5 < waited < 30.0, waited             # bounded waits, not a hang
     assert all(torch.equal(a, b) for a, b in zip(call(), want))
     ops.device_status()
+
+
+# ------------------------------------------------------------------------ gated feed-forward
+@pytest.mark.parametrize("T", [3, 200, 2321])
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_gates_beyond_their_range_have_their_gradient(T, act, dtype):
+    # One hidden column has gates of -98304, which fp16 saves as -infinity, or (bf16) of -2^70,
+    # whose square is not in fp32. act and act' are 0 there as they are at -200, so every result
+    # has the bits that gates of -200 give; at the opposite gates act' is 1 as at 200.
+    d, f = (72, 136) if T < 2321 else (2088, 2632)
+    x, W1, W3, W2, dout = ffn_case(T, d, f, dtype, 46)
+    first, big = (2.0, 98304.0) if dtype == "fp16" else (2.0 ** 35, 2.0 ** 70)
+    x[:, 0] = first
+    W1[:, 0], W3[:, 0], W1[5] = 0, 0, 0
+
+    def step(gate_value, needs):
+        W1[5, 0] = gate_value / first
+        out, gate, up = ops.gated_ffn_forward(x, W1, W3, W2, act, save=True)
+        want = gate_value if dtype == "bf16" or abs(gate_value) < 65504 else \
+            float("inf") * gate_value
+        assert (gate[:, 5] == want).all()
+        return [out, *ops.gated_ffn_backward(dout, x, W1, W3, W2, gate, up, act, needs)]
+
+    near = 200.0 if dtype == "fp16" else 2.0 ** 8
+    for a, b in zip(step(-big, (False, True, True, True)), step(-near, (False, True, True, True))):
+        assert a is b is None or (torch.isfinite(a).all() and torch.equal(a, b))
+    far, ref = step(big, (False, True, False, False)), step(near, (False, True, False, False))
+    assert torch.isfinite(far[2]).all() and torch.equal(far[2], ref[2])
+    # dx: the column's dgate and dup are 0, its weights finite
+    dx = step(-big, (True, False, False, False))[1]
+    assert torch.isfinite(dx).all()
+    W1[5, 0] = 0
+    gate, up = ops.gated_ffn_forward(x, W1, W3, W2, act, save=True)[1:]
+    gate[:, 5] = -near
+    W1[5, 0] = -big / first
+    assert torch.equal(dx, ops.gated_ffn_backward(dout, x, W1, W3, W2, gate, up, act,
+                                                  (True, False, False, False))[0])
