@@ -9,7 +9,8 @@ from mixture_experts_ffn_expert_b200 import ops
 from mixture_experts_ffn_expert_b200.binding import MoEError, load_library
 from oracle import ops_oracle as O
 from test_ops_edges_cpu import Wrapper
-from test_ops_gpu import (DT, K, U32, close, drop_tol, f64, ffn_bounds, ffn_case, gen,
+from test_ops_gpu import test_norm as base_norm
+from test_ops_gpu import (DT, K, U32, check_ffn, close, drop_tol, f64, ffn_bounds, ffn_case, gen,
                           norm_bounds, randn, unit)
 
 pytestmark = pytest.mark.gpu
@@ -436,3 +437,64 @@ def test_gates_beyond_their_range_have_their_gradient(T, act, dtype):
     W1[5, 0] = -big / first
     assert torch.equal(dx, ops.gated_ffn_backward(dout, x, W1, W3, W2, gate, up, act,
                                                   (True, False, False, False))[0])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("rows,cols", [(100001, 1), (60000, 3), (50000, 8), (30011, 17), (9000, 40)])
+def test_norm_many_short_rows(rows, cols, dtype):
+    base_norm(rows, cols, dtype, dtype, "layer")
+    base_norm(rows, cols, dtype, "fp32", "rms")
+
+
+@pytest.mark.parametrize("cols", [8192, 8191])
+def test_norm_beyond_32_bits(cols):
+    # 4.9e9 elements; the gradient of the weights comes from a few rows, the others' dy is 0
+    rows = 600_000
+    torch.manual_seed(0)
+    x = torch.empty((rows, cols), dtype=torch.bfloat16, device="cuda").normal_()
+    at = [0, 1, 299_999, 524_288, 524_289, rows - 2, rows - 1]
+    dy = torch.zeros_like(x)
+    some = randn(gen(47), len(at), cols)
+    dy[at] = some
+    w = randn(gen(48), cols, shift=1.0)
+    y, mean, rstd = ops.norm_forward(x, w, save=True)
+    want = norm_bounds(f64(x[at]), f64(w), None, f64(some), x.dtype, x.dtype, "layer", 1e-5)
+    close(y[at], *want[0], "y")
+    del y
+    dx, dw, db = ops.norm_backward(dy, x, w, mean, rstd, bias=True)
+    close(dx[at], *want[1], "dx")
+    close(dw, *want[2], "dweight")
+    close(db, *want[3], "dbias")
+    keep = torch.ones(rows, dtype=torch.bool, device="cuda")
+    keep[at] = False
+    assert dx.abs().amax(1)[keep].max() == 0
+
+
+@pytest.mark.parametrize("T,d,f,dtype,act", [
+    (100_003, 8, 8, "bf16", "silu"), (40_000, 64, 16, "fp16", "gelu"), (3, 16384, 8, "bf16", "gelu"),
+    (130, 8, 16384, "fp16", "silu"), (257, 20000, 24, "bf16", "silu"), (1, 8, 30000, "bf16", "silu"),
+    (4099, 8, 1000, "bf16", "gelu")])
+def test_gated_ffn_lopsided_shapes(T, d, f, dtype, act):
+    check_ffn(T, d, f, dtype, act)
+
+
+def test_gated_ffn_beyond_32_bits():
+    # 4.3e9 hidden elements; gradients from a few tokens, the others' dout is 0
+    T, d, f = 300_001, 64, 14336
+    x, W1, W3, W2, _ = ffn_case(8, d, f, "bf16", 49)
+    at = [0, 1, 127, 149_999, 299_000, 299_592, T - 2, T - 1]
+    torch.manual_seed(1)
+    xl = torch.empty((T, d), dtype=torch.bfloat16, device="cuda").normal_()
+    xl[at] = x
+    dout = torch.zeros_like(xl)
+    some = randn(gen(50), 8, d, scale=0.25)
+    dout[at] = some
+    out, gate, up = ops.gated_ffn_forward(xl, W1, W3, W2, save=True)
+    grads = ops.gated_ffn_backward(dout, xl, W1, W3, W2, gate, up)
+    ops.device_status()
+    want = ffn_bounds(*(f64(t) for t in (x, W1, W3, W2, some)), "silu", x.dtype)
+    close(out[at], *want["out"], "out")
+    close(grads[0][at], *want["dx"], "dx")
+    # T products a reduction, of which 8 are not 0: adding zeros rounds nothing
+    for name, got in zip(("dW1", "dW3", "dW2"), grads[1:]):
+        close(got, *want[name], name)
