@@ -382,6 +382,7 @@ PyObject* dropout_add(PyObject*, PyObject* const* a, Py_ssize_t given) {
     const int dt = dtype_of(x);
     if (x.dim() == 0) refuse("x must have at least one dimension");
     const double p = number(a[2], "p");
+    if (!(p >= 0.0 && p <= 1.0)) refuse("p must lie in [0, 1]");      // also of an empty tensor
     const uint64_t* rng = nullptr;
     if (!(p == 0.0 && a[3] == Py_None)) {
       const at::Tensor& r = cuda_tensor(a[3], "rng");

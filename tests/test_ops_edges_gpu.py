@@ -498,3 +498,12 @@ def test_gated_ffn_beyond_32_bits():
     # T products a reduction, of which 8 are not 0: adding zeros rounds nothing
     for name, got in zip(("dW1", "dW3", "dW2"), grads[1:]):
         close(got, *want[name], name)
+
+
+def test_dropout_refuses_its_probability_for_empty_tensors_too():
+    x = torch.zeros((0, 8), device="cuda")
+    rng = torch.tensor([1, 2], device="cuda")
+    for p in (-0.5, 1.5, float("nan")):
+        with pytest.raises(MoEError):
+            ops.dropout_add_forward(x, None, p, rng)
+    assert ops.dropout_add_forward(x, None, 0.5, rng).shape == (0, 8)
