@@ -317,8 +317,10 @@ enum { MOE_ACT_SILU = 0, MOE_ACT_GELU = 1 };
  * RMS-normalised.) weight (cols) and bias (cols) may be NULL (1 and 0) and have
  * x's dtype or fp32 (wdtype); an RMS norm takes no bias. mean and rstd (rows,
  * fp32) are written when non-NULL, for the backward pass (mean: layer norm
- * only). Any cols up to 2^24, any row strides >= cols, any element-aligned
- * pointers; 16-byte aligned rows run faster. y may be x itself (equal strides). */
+ * only). Statistics and sums are fp32, the mean summed from the row's first
+ * element, so that rows far from zero lose nothing; one rounding, on the store.
+ * Any cols up to 2^24, any row strides >= cols, any element-aligned pointers;
+ * 16-byte aligned rows run faster. y may be x itself (equal strides). */
 int moe_norm_forward(int kind, int dtype, int wdtype, int64_t rows, int64_t cols,
                      const void* x, int64_t ldx, const void* weight, const void* bias,
                      double eps, void* y, int64_t ldy, float* mean, float* rstd,
@@ -345,9 +347,11 @@ int moe_norm_backward(int kind, int dtype, int wdtype, int64_t rows, int64_t col
  * x (T, d), W1 and W3 (f, d), W2 (d, f) contiguous, out (T, d); bf16 or fp16,
  * fp32 accumulation, h rounded to the type between the two products. act is
  * SiLU, or GELU in its tanh form. gate and up (T, f), both or neither, receive
- * the pre-activations for the backward pass. d and f are multiples of 8; row
- * strides are multiples of 8; pointers are 16-byte aligned; the workspace is
- * 256-byte aligned, moe_gated_ffn_workspace_bytes(T, d, f, 0) bytes. */
+ * the pre-activations for the backward pass, rounded to the type. In fp16 what
+ * passes 65504 becomes infinite: h (also where out would not), and the saved gate
+ * and up. d and f are multiples of 8; row strides are multiples of 8; pointers are
+ * 16-byte aligned; the workspace is 256-byte aligned,
+ * moe_gated_ffn_workspace_bytes(T, d, f, 0) bytes. */
 size_t moe_gated_ffn_workspace_bytes(int64_t T, int64_t d, int64_t f, int backward);
 int moe_gated_ffn_forward(int act, int dtype, int64_t T, int64_t d, int64_t f,
                           const void* x, int64_t ldx, const void* W1, const void* W3,
@@ -358,8 +362,10 @@ int moe_gated_ffn_forward(int act, int dtype, int64_t T, int64_t d, int64_t f,
  *   dh = dout W2,  dgate = dh * up * act'(gate),  dup = dh * act(gate)
  *   dx = dgate W1 + dup W3,  dW1 = dgate^T x,  dW3 = dup^T x,  dW2 = dout^T h
  * Any of dx, dW1, dW3, dW2 may be NULL (not computed); the weight gradients are
- * contiguous, overwritten (zero when T = 0). dgate, dup and h are rounded to
- * the type between the products. Workspace as above with backward = 1. */
+ * contiguous, overwritten (zero when T = 0). h is computed again from the saved
+ * gate and up; dgate, dup and h are rounded to the type between the products (in
+ * fp16 infinite beyond 65504). act and act' of an infinite gate are their limits,
+ * so a gate below the type's range adds 0. Workspace as above with backward = 1. */
 int moe_gated_ffn_backward(int act, int dtype, int64_t T, int64_t d, int64_t f,
                            const void* dout, int64_t lddout, const void* x, int64_t ldx,
                            const void* W1, const void* W3, const void* W2, const void* gate,

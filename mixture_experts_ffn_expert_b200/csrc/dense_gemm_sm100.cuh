@@ -14,6 +14,11 @@
 //             dW1, dW3 A = dgate / dup (m), B = x (n)
 //             dW2      A = dout (m), B = h (n)
 //
+// What is rounded to 16 bits between the products: h, dgate and dup because they are operands
+// of the next; the saved gate and up by choice (see the forward epilogue). The backward pass
+// computes h again from the saved gate and up instead of keeping a third matrix, so the h of
+// dW2 differs from the forward's by those two roundings. In fp16 what passes 65504 is infinite.
+//
 // Warp roles: warp 0 loads A, warp 6 loads B, one thread of warp 1 issues the MMAs,
 // warps 2-5 run the epilogue from TMEM while the next tile's MMAs fill the other
 // accumulator. PAIR: a cluster of two CTAs computes a 256 x 256 tile (cta_group::2, each
@@ -495,6 +500,10 @@ __global__ void __launch_bounds__(kDgThreads, 1)
             const float* ua = reinterpret_cast<const float*>(u) + v * 8;
 #pragma unroll
             for (int j = 0; j < 8; ++j) h[j] = act_value(ga[j], P.act) * ua[j];
+            // h is rounded because the next product's operands are of 16 bits. gate and up
+            // are no operands: they are saved in the type to halve their bytes (4096 tokens,
+            // f=14336: 235 MB of activations kept and 470 written and read, instead of twice
+            // that), at the price of one rounding more in each gradient.
             packed[0][v] = pack8<T>(h);
             packed[1 % Cfg::kOuts][v] = pack8<T>(ga);
             packed[2 % Cfg::kOuts][v] = pack8<T>(ua);

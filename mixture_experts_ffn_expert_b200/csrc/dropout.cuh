@@ -162,7 +162,10 @@ __global__ void __launch_bounds__(256, 4) dropout_flat_kernel(const DropoutParam
 }
 
 // Any strides and alignment: a thread takes the four elements of one Philox block,
-// element by element.
+// element by element, with one 64-bit division for the block's row (8192 x 7168 bf16, rows
+// padded or starting at an odd element: 178 us forward and 154 backward, where the contiguous
+// kernel takes 55 and 51; 777 x 1001 fp32 4.7 and 2.7). It is there so that no layout is refused;
+// a program that draws over large padded tensors is better off with contiguous ones.
 template <typename T, bool RES, int MODE>
 __global__ void __launch_bounds__(256) dropout_strided_kernel(const DropoutParams P) {
   pdl_wait();

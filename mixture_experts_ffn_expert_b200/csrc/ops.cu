@@ -41,11 +41,14 @@ const char* check_rows(int64_t rows, int64_t cols) {
 }
 bool bad_stride(int64_t rows, int64_t cols, int64_t ld) { return rows > 1 && ld < cols; }
 
+// SMs of a B200, for the thresholds below (measured on one); grids ask the device.
+constexpr int kB200Sms = 148;
+
 constexpr int64_t kMaxRows = (1LL << 31) - 1;
 constexpr int64_t kMaxCols = 1LL << 24;
 
 // ------------------------------------------------------------------ norm
-constexpr int kNormBlocks = 296;        // blocks (partial rows) of a backward pass, two an SM
+constexpr int kNormBlocks = 2 * kB200Sms;   // blocks (partial rows) of a backward pass at most
 
 int round32(int64_t v) { return static_cast<int>((v + 31) / 32 * 32); }
 
@@ -61,18 +64,18 @@ cudaError_t launch_norm_forward(const moe::NormParams& P, int group, cudaStream_
 // rows of 4097 to 8192 (forward, 300 x 7168 bf16: 6.3 us, 7.8 with a block a row) and for
 // unaligned rows above 4096 (300 x 7001 bf16: 10.1 and 14.9).
 int64_t tile_rows_forward(int cols, bool vec) {
-  return cols > 4096 && (cols <= 8192 || !vec) ? 296 : 592;
+  return (cols > 4096 && (cols <= 8192 || !vec) ? 2 : 4) * kB200Sms;
 }
 // Backward: with two also from 256 to 1024 vectors a row (300 x 2048 bf16: 11.8 us, 13.7 with
 // a block a row), and always for unaligned rows of 4097 to 8192 (1 x 7001 bf16: 9.6 us; a
 // block a row would hold so many elements a thread that they spill, 20.6).
 int64_t tile_rows_backward(int cols, bool vec, int vectors) {
-  if (vec) return vectors >= 256 && vectors <= 1024 ? 296 : 592;
-  return cols > 4096 && cols <= 8192 ? 1 : 592;
+  if (vec) return (vectors >= 256 && vectors <= 1024 ? 2 : 4) * kB200Sms;
+  return cols > 4096 && cols <= 8192 ? 1 : 4 * kB200Sms;
 }
 constexpr size_t kTileSmem = 208 * 1024;
 // 16 column warps beside the 8 row warps (with 8, 4096 x 7168 bf16 forward took 36 us
-// instead of 26 and the backward pass up to 30% longer).
+// where it took 26 and the backward pass up to 30% longer).
 constexpr int kColumnWarps = 16;
 
 // Rows a tile and slots, for `planes` matrices (x, and dy in the backward pass): three
@@ -243,8 +246,9 @@ cudaError_t norm_backward_any(const moe::NormParams& P, bool vec, bool contiguou
   } else if (P.cols <= 4096) {
     return launch_norm_backward<T, 1, 4, RMS, GRADW>(P, round32((P.cols + 3) / 4), blocks, st);
   }
-  // Wider rows from global memory, three passes (300 x 16384 fp32: 41 us; held in the
-  // registers of a block, spilling, 90).
+  // Wider rows from global memory, three passes, element by element (300 x 16384 fp32: 40 us;
+  // held in the registers of a block, spilling, 90. 3000 x 16384 fp32: 275 us, 600 x 70000: 316,
+  // where reading x and dy and writing dx once would be 90 and 77).
   cudaError_t e = cudaSuccess;
   if (GRADW) {                          // before dx, which may overwrite dy
     *blocks = static_cast<int>(P.rows < 32 ? P.rows : 32);
@@ -309,7 +313,7 @@ cudaError_t launch_dropout(moe::DropoutParams P, bool flat, cudaStream_t st) {
     // Four vectors a thread once that still leaves two rounds of blocks for every SM; below,
     // one each (128 x 2048 bf16: 1.5 us against 2.3 with four).
     cudaError_t e;
-    if (vecs >= 8 * 148 * 1024)
+    if (vecs >= int64_t(8) * kB200Sms * 1024)
       e = launch_overlapped(moe::dropout_flat_kernel<T, RES, MODE, 4>,
                             dim3(unsigned((vecs + 1023) / 1024)), dim3(256), 0, st, 1, P);
     else

@@ -144,9 +144,11 @@ def gated_ffn_forward(x: torch.Tensor, W1: torch.Tensor, W3: torch.Tensor, W2: t
                       activation: str = "silu", save: bool = False):
     """(act(x W1^T) * (x W3^T)) W2^T over x (..., d), bf16 or fp16.
 
-    W1 and W3 are (f, d), W2 (d, f), contiguous, d and f multiples of 8; activation is
-    "silu" or "gelu" (tanh form). Returns out, or with ``save`` (out, gate, up): the (T, f)
-    pre-activations for ``gated_ffn_backward``.
+    W1 and W3 are (f, d), W2 (d, f), contiguous and 16-byte aligned, d and f multiples of 8;
+    activation is "silu" or "gelu" (tanh form). Returns out, or with ``save`` (out, gate, up):
+    the (T, f) pre-activations for ``gated_ffn_backward``. Products accumulate in fp32; the
+    hidden layer and the saved pre-activations are rounded to x's type (fp16: infinite beyond
+    65504).
     """
     return (_MODULE or _host()).gated_ffn_forward(x, W1, W3, W2, activation, save)
 
