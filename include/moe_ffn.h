@@ -347,15 +347,14 @@ int moe_norm_backward(int kind, int dtype, int wdtype, int64_t rows, int64_t col
  * x (T, d), W1 and W3 (f, d), W2 (d, f) contiguous, out (T, d); bf16 or fp16,
  * fp32 accumulation, h rounded to the type between the two products. act is
  * SiLU, or GELU in its tanh form. gate and up (T, f), both or neither, receive
- * the pre-activations for the backward pass, rounded to the type. In fp16 what
- * passes 65504 becomes infinite: h (also where out would not), and the saved gate
- * and up. d and f are multiples of 8; row strides are multiples of 8; pointers are
+ * the pre-activations for the backward pass, in fp32. In fp16 an h beyond 65504
+ * becomes infinite (also where out would not). d and f are multiples of 8; row strides are multiples of 8; pointers are
  * 16-byte aligned; the workspace is 256-byte aligned,
  * moe_gated_ffn_workspace_bytes(T, d, f, 0) bytes. */
 size_t moe_gated_ffn_workspace_bytes(int64_t T, int64_t d, int64_t f, int backward);
 int moe_gated_ffn_forward(int act, int dtype, int64_t T, int64_t d, int64_t f,
                           const void* x, int64_t ldx, const void* W1, const void* W3,
-                          const void* W2, void* out, int64_t ldo, void* gate, void* up,
+                          const void* W2, void* out, int64_t ldo, float* gate, float* up,
                           void* workspace, size_t workspace_bytes, void* stream);
 
 /* Backward of moe_gated_ffn_forward from dout (T, d) and the saved gate and up:
@@ -364,12 +363,11 @@ int moe_gated_ffn_forward(int act, int dtype, int64_t T, int64_t d, int64_t f,
  * Any of dx, dW1, dW3, dW2 may be NULL (not computed); the weight gradients are
  * contiguous, overwritten (zero when T = 0). h is computed again from the saved
  * gate and up; dgate, dup and h are rounded to the type between the products (in
- * fp16 infinite beyond 65504). act and act' of an infinite gate are their limits,
- * so a gate below the type's range adds 0. Workspace as above with backward = 1. */
+ * fp16 infinite beyond 65504). Workspace as above with backward = 1. */
 int moe_gated_ffn_backward(int act, int dtype, int64_t T, int64_t d, int64_t f,
                            const void* dout, int64_t lddout, const void* x, int64_t ldx,
-                           const void* W1, const void* W3, const void* W2, const void* gate,
-                           const void* up, void* dx, int64_t lddx, void* dW1, void* dW3,
+                           const void* W1, const void* W3, const void* W2, const float* gate,
+                           const float* up, void* dx, int64_t lddx, void* dW1, void* dW3,
                            void* dW2, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Residual add with dropout: out[e] = residual[e] + (keep(e) ? x[e] / (1 - p) : 0)

@@ -7,17 +7,18 @@
 // so no operand is ever transposed in memory.
 //
 // One launch runs a list of products (a persistent kernel walks all their tiles):
-//   forward   gate/up  A = x (k), B = W1 and W3 (k)     epilogue act(gate) * up
+//   forward   gate/up  A = x (k), B = W1 and W3 (k)     epilogue act(gate) * up; gate, up saved
 //             down     A = h (k), B = W2 (k)            plain
 //   backward  dh       A = dout (k), B = W2 (n)         epilogue dgate, dup, h
 //             dx       A = dgate then dup (k), B = W1 then W3 (n); one reduction over 2f
 //             dW1, dW3 A = dgate / dup (m), B = x (n)
 //             dW2      A = dout (m), B = h (n)
 //
-// What is rounded to 16 bits between the products: h, dgate and dup because they are operands
-// of the next; the saved gate and up by choice (see the forward epilogue). The backward pass
-// computes h again from the saved gate and up instead of keeping a third matrix, so the h of
-// dW2 differs from the forward's by those two roundings. In fp16 what passes 65504 is infinite.
+// h, dgate and dup are rounded to 16 bits between the products because they are operands of the
+// next. gate and up are none: they are saved in fp32, so that a gradient has one rounding on its
+// way beside its own (saved in 16 bits, which takes 470 MB less traffic for 4096 tokens and
+// f=14336, the gradients' errors were twice a rounding's). The backward pass computes h again
+// from them instead of keeping a third matrix. In fp16 what passes 65504 is infinite.
 //
 // Warp roles: warp 0 loads A, warp 6 loads B, one thread of warp 1 issues the MMAs,
 // warps 2-5 run the epilogue from TMEM while the next tile's MMAs fill the other
@@ -33,7 +34,7 @@
 
 namespace moe {
 
-enum { kGemmPlain = 0, kGemmGluForward = 1, kGemmGluBackward = 2 };
+enum { kGemmPlain = 0, kGemmGluForward = 1, kGemmGluBackward = 2, kGemmGluForwardSave = 3 };
 enum { kActSilu = 0, kActGelu = 1 };
 
 constexpr int kDgThreads = 224;
@@ -49,15 +50,20 @@ constexpr int kDgStageBytes = 2 * kDgTileBytes;
 // dh product of a 4096 x 4096 x 14336 step, which reads two and writes three matrices in
 // its epilogue, took 490 us that way.) Plain products use chunks of 64 columns and four
 // buffers (with a short reduction, as of the weights' gradients over few tokens, the stores
-// are the kernel), those with three outputs 32 columns and two.
+// are the kernel), gate/up 32 columns and four, with the pre-activations saved 16 columns (one
+// buffer of 16 and two of 32 bits) and three, dh 32 columns of three outputs and two.
 template <int EPI>
 struct DenseCfg {
-  static constexpr int kChunk = EPI == 0 ? 64 : 32;
-  static constexpr int kOuts = EPI == 0 ? 1 : 3;
-  static constexpr int kSets = EPI == 0 ? 4 : 2;
+  static constexpr bool kGlu = EPI == kGemmGluForward || EPI == kGemmGluForwardSave;
+  static constexpr bool kSave = EPI == kGemmGluForwardSave;
+  static constexpr int kChunk = EPI == kGemmPlain ? 64 : kSave ? 16 : 32;
+  static constexpr int kOuts = EPI == kGemmPlain || EPI == kGemmGluForward ? 1 : 3;
+  static constexpr int kSets = EPI == kGemmGluBackward ? 2 : kSave ? 3 : 4;
   static constexpr int kStages = 5;
-  static constexpr int kBufBytes = 128 * kChunk * 2;
-  static constexpr int kSetBytes = kOuts * kBufBytes;
+  static constexpr int kBufBytes = 128 * kChunk * 2;            // one 16-bit output's chunk
+  // start of output o's chunk in a set (saved ones are twice as large as the first)
+  static constexpr int out_at(int o) { return o == 0 ? 0 : kSave ? (2 * o - 1) * kBufBytes : o * kBufBytes; }
+  static constexpr int kSetBytes = kSave ? 5 * kBufBytes : kOuts * kBufBytes;
   static constexpr size_t kSmem =
       1024 + size_t(kStages) * kDgStageBytes + kSets * size_t(kSetBytes) + 256;
   static_assert(kSmem <= 227 * 1024, "one block's shared memory");
@@ -77,8 +83,7 @@ struct DenseParams {
   int n_problems, total_tiles, n_maps;
   int first_tiles;                  // tiles of problem 0 (the costly ones)
   int extra;                        // see tile_of
-  const void *gate, *up;            // dh: the saved pre-activations (M, N)
-  int save;                         // gate/up: store them
+  const float *gate, *up;           // dh: the saved pre-activations (M, N)
   int act;
   int test_withhold;                // test hook: worker 0 withholds its first stage's copy of A
   int* status;
@@ -175,9 +180,9 @@ __device__ __forceinline__ float act_value(float a, int act) {
   const float z = act == kActSilu ? a : 1.5957691216057308f * (a + 0.044715f * a * a * a);
   return a * __fdividef(1.0f, 1.0f + __expf(-z));
 }
-// The gate is a saved one, infinite where it passed the 16-bit type's range; below -1e12 it is
-// taken as -1e12, and for the derivative above 1e12 as 1e12 (s is exactly 0 or 1 long before), so
-// that 0 times infinity does not make a NaN of a gradient that is 0 or 1.
+// A gate may be as large as fp32 holds, or infinite: below -1e12 it is taken as -1e12, and for
+// the derivative above 1e12 as 1e12 (s is exactly 0 or 1 long before), so that 0 times infinity
+// does not make a NaN of a gradient that is 0 or 1.
 __device__ __forceinline__ void act_value_grad(float a, int act, float& v, float& d) {
   a = a < -1e12f ? -1e12f : a;
   const float b = a > 1e12f ? 1e12f : a;
@@ -218,11 +223,14 @@ __device__ __forceinline__ void epilogue_barrier() {
   asm volatile("bar.sync 1, 128;" ::: "memory");
 }
 
-// Byte offset of the 16-byte piece c of row r in a staged chunk (the 128- or 64-byte TMA
-// swizzle for rows of 128 or 64 bytes).
-template <int CHUNK>
+// Byte offset of the 16-byte piece c of row r in a staged chunk (the 128-, 64- or 32-byte TMA
+// swizzle for rows of as many bytes).
+template <int ROW_BYTES>
 __device__ __forceinline__ uint32_t staged(int r, int c) {
-  return CHUNK == 64 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+  static_assert(ROW_BYTES == 128 || ROW_BYTES == 64 || ROW_BYTES == 32, "a swizzle's row");
+  return ROW_BYTES == 128  ? r * 128 + ((c ^ (r & 7)) << 4)
+         : ROW_BYTES == 64 ? r * 64 + ((c ^ ((r >> 1) & 3)) << 4)
+                           : r * 32 + ((c ^ ((r >> 2) & 1)) << 4);
 }
 __device__ __forceinline__ void st_shared_16(uint32_t addr, uint4 v) {
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z),
@@ -239,7 +247,8 @@ __global__ void __launch_bounds__(kDgThreads, 1)
   constexpr int kTileM = PAIR ? 256 : 128;
   constexpr int kAcc = PAIR ? 256 : 128;            // accumulator columns of a tile
   constexpr int kTmem = 2 * kAcc;
-  constexpr int kOutCols = EPI == kGemmGluForward ? kAcc / 2 : kAcc;
+  constexpr bool kGlu = Cfg::kGlu;
+  constexpr int kOutCols = kGlu ? kAcc / 2 : kAcc;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -311,12 +320,12 @@ __global__ void __launch_bounds__(kDgThreads, 1)
         const int mn = is_a ? q.a_mn : q.b_mn;
         // first m or n of this CTA's 128 rows of the operand
         int row0 = is_a ? tc.m * kTileM + half * 128 : tc.n * kOutCols;
-        if (!is_a && PAIR && EPI != kGemmGluForward) row0 += half * 128;
+        if (!is_a && PAIR && !kGlu) row0 += half * 128;
         for (int seg = 0; seg < 2 && ok; ++seg) {
           const int nkb = q.kb[seg];
           const CUtensorMap* map =
               &maps.m[is_a ? q.map_a[seg]
-                           : (PAIR && EPI == kGemmGluForward ? q.map_b[half] : q.map_b[seg])];
+                           : (PAIR && kGlu ? q.map_b[half] : q.map_b[seg])];
           const CUtensorMap* map1 = &maps.m[q.map_b[1]];
           for (int kb = 0; kb < nkb; ++kb) {
             ok = mbar_wait(smem_u32(&empty_bar[s]), ph ^ 1u, s_abort);
@@ -342,7 +351,7 @@ __global__ void __launch_bounds__(kDgThreads, 1)
             } else if (mn) {
               tma_load_2d(dst, map, fb, row0, k0);
               tma_load_2d(dst + 8192, map, fb, row0 + 64, k0);
-            } else if (EPI == kGemmGluForward && !is_a) {
+            } else if (kGlu && !is_a) {
               tma_load_2d(dst, map, fb, k0, row0);          // 64 rows of W1, 64 of W3
               tma_load_2d(dst + 8192, map1, fb, k0, row0);
             } else {
@@ -455,20 +464,23 @@ __global__ void __launch_bounds__(kDgThreads, 1)
       const int col0 = tc.n * kOutCols;
       const uint32_t tbase = lane_base + static_cast<uint32_t>(acc * kAcc);
       const int cols = min(kOutCols, q.N - col0);
-      // dh: the saved pre-activations of a chunk are loaded one chunk ahead
-      uint4 g4[4], u4[4];
-      auto load_saved = [&](int c) {
-        const long long at = row * q.N + col0 + c;
+      // dh: the saved pre-activations of a chunk are loaded one chunk ahead, 8 columns (v) at
+      // a time as the present chunk's are used
+      float4 g4[8], u4[8];
+      auto load_saved = [&](int c, int v) {
+        const long long at = row * q.N + col0 + c + v * 8;
+        const bool in = row_ok && c + v * 8 < cols;
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const bool in = row_ok && c + v * 8 < cols;
-          g4[v] = in ? *reinterpret_cast<const uint4*>(static_cast<const T*>(P.gate) + at + v * 8)
-                     : make_uint4(0, 0, 0, 0);
-          u4[v] = in ? *reinterpret_cast<const uint4*>(static_cast<const T*>(P.up) + at + v * 8)
-                     : make_uint4(0, 0, 0, 0);
+        for (int i = 2 * v; i < 2 * v + 2; ++i) {
+          const long long e = at + (i & 1) * 4;
+          g4[i] = in ? *reinterpret_cast<const float4*>(P.gate + e) : make_float4(0, 0, 0, 0);
+          u4[i] = in ? *reinterpret_cast<const float4*>(P.up + e) : make_float4(0, 0, 0, 0);
         }
       };
-      if (EPI == kGemmGluBackward) load_saved(0);
+      if (EPI == kGemmGluBackward) {
+#pragma unroll
+        for (int v = 0; v < 4; ++v) load_saved(0, v);
+      }
       bool ok = mbar_wait(smem_u32(&tfull_bar[acc]), acc_ph, s_abort);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok && lane == 0) raise_abort(s_abort, P.status);
@@ -486,40 +498,85 @@ __global__ void __launch_bounds__(kDgThreads, 1)
 #pragma unroll 1
       for (int c = 0; c < cols; c += kCh) {
         const uint32_t buf = stage0 + set * Cfg::kSetBytes;
-        uint32_t a[32];
-        uint4 packed[Cfg::kOuts][kCh / 8];
-        if (EPI == kGemmGluForward) {
-          uint32_t u[32];
+        constexpr int kRowBytes = kCh * 2;
+        // this set's previous stores (kSets chunks ago) have read it
+        auto set_free = [&] {
+          if (storer) bulk_wait_read<Cfg::kSets - 1>();
+          __syncwarp();
+          epilogue_barrier();
+        };
+        // after the last chunk's loads the accumulator is read: the next tile may have it
+        auto release = [&] {
+          if (c + kCh < cols) return;
+          tc_fence_before_sync();
+          if (PAIR && !leader)
+            mbar_arrive_cluster(mapa_shared(smem_u32(&tempty_bar[acc]), 0));
+          else
+            mbar_arrive(smem_u32(&tempty_bar[acc]));
+        };
+        if constexpr (EPI == kGemmGluForward) {
+          uint32_t a[32], u[32];
           tmem_ld_32cols(tbase + c, a);
           tmem_ld_32cols(tbase + kOutCols + c, u);
           tmem_ld_wait();
+          release();
+          uint4 packed[4];
 #pragma unroll
           for (int v = 0; v < 4; ++v) {
             float h[8];
-            const float* ga = reinterpret_cast<const float*>(a) + v * 8;
-            const float* ua = reinterpret_cast<const float*>(u) + v * 8;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) h[j] = act_value(ga[j], P.act) * ua[j];
-            // h is rounded because the next product's operands are of 16 bits. gate and up
-            // are no operands: they are saved in the type to halve their bytes (4096 tokens,
-            // f=14336: 235 MB of activations kept and 470 written and read, instead of twice
-            // that), at the price of one rounding more in each gradient.
-            packed[0][v] = pack8<T>(h);
-            packed[1 % Cfg::kOuts][v] = pack8<T>(ga);
-            packed[2 % Cfg::kOuts][v] = pack8<T>(ua);
+            for (int j = 0; j < 8; ++j)
+              h[j] = act_value(__uint_as_float(a[v * 8 + j]), P.act) *
+                     __uint_as_float(u[v * 8 + j]);
+            packed[v] = pack8<T>(h);
           }
-        } else if (EPI == kGemmGluBackward) {
+          set_free();
+#pragma unroll
+          for (int v = 0; v < 4; ++v) st_shared_16(buf + staged<kRowBytes>(r, v), packed[v]);
+        } else if constexpr (EPI == kGemmGluForwardSave) {
+          uint32_t a[2][8], u[2][8];
+#pragma unroll
+          for (int v = 0; v < 2; ++v) {
+            tmem_ld_8cols(tbase + c + v * 8, a[v]);
+            tmem_ld_8cols(tbase + kOutCols + c + v * 8, u[v]);
+          }
+          tmem_ld_wait();
+          release();
+          uint4 packed[2];
+#pragma unroll
+          for (int v = 0; v < 2; ++v) {
+            float h[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              h[j] = act_value(__uint_as_float(a[v][j]), P.act) * __uint_as_float(u[v][j]);
+            packed[v] = pack8<T>(h);
+          }
+          set_free();
+#pragma unroll
+          for (int v = 0; v < 2; ++v) st_shared_16(buf + staged<kRowBytes>(r, v), packed[v]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t* ga = &a[i >> 1][(i & 1) * 4];
+            const uint32_t* ua = &u[i >> 1][(i & 1) * 4];
+            const uint32_t at = buf + staged<2 * kRowBytes>(r, i);
+            st_shared_16(at + Cfg::out_at(1), make_uint4(ga[0], ga[1], ga[2], ga[3]));
+            st_shared_16(at + Cfg::out_at(2), make_uint4(ua[0], ua[1], ua[2], ua[3]));
+          }
+        } else if constexpr (EPI == kGemmGluBackward) {
+          uint32_t a[32];
           tmem_ld_32cols(tbase + c, a);
           tmem_ld_wait();
+          release();
+          set_free();
 #pragma unroll
           for (int v = 0; v < 4; ++v) {
-            const uint32_t gw[4] = {g4[v].x, g4[v].y, g4[v].z, g4[v].w};
-            const uint32_t uw[4] = {u4[v].x, u4[v].y, u4[v].z, u4[v].w};
             float dg[8], du[8], h[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-              const float2 gp = unpack2<T>(gw[j >> 1]), upv = unpack2<T>(uw[j >> 1]);
-              const float g = j & 1 ? gp.y : gp.x, u = j & 1 ? upv.y : upv.x;
+              const float4 gp = g4[2 * v + (j >> 2)], upv = u4[2 * v + (j >> 2)];
+              const int k = j & 3;
+              const float g = k == 0 ? gp.x : k == 1 ? gp.y : k == 2 ? gp.z : gp.w;
+              const float u = k == 0 ? upv.x : k == 1 ? upv.y : k == 2 ? upv.z : upv.w;
               const float dh = __uint_as_float(a[v * 8 + j]);
               float val, der;
               act_value_grad(g, P.act, val, der);
@@ -527,49 +584,35 @@ __global__ void __launch_bounds__(kDgThreads, 1)
               du[j] = dh * val;
               h[j] = val * u;
             }
-            packed[0][v] = pack8<T>(h);
-            packed[1 % Cfg::kOuts][v] = pack8<T>(dg);
-            packed[2 % Cfg::kOuts][v] = pack8<T>(du);
+            if (c + kCh < cols) load_saved(c + kCh, v);
+            const uint32_t at = buf + staged<kRowBytes>(r, v);
+            st_shared_16(at, pack8<T>(h));
+            st_shared_16(at + Cfg::out_at(1), pack8<T>(dg));
+            st_shared_16(at + Cfg::out_at(2), pack8<T>(du));
           }
-          if (c + kCh < cols) load_saved(c + kCh);
         } else {
+          uint4 packed[8];
 #pragma unroll
-          for (int hh = 0; hh < kCh / 32; ++hh) {
+          for (int hh = 0; hh < 2; ++hh) {
+            uint32_t a[32];
             tmem_ld_32cols(tbase + c + hh * 32, a);
             tmem_ld_wait();
 #pragma unroll
             for (int v = 0; v < 4; ++v)
-              packed[0][(hh * 4 + v) % (kCh / 8)] =
-                  pack8<T>(reinterpret_cast<const float*>(a) + v * 8);
+              packed[hh * 4 + v] = pack8<T>(reinterpret_cast<const float*>(a) + v * 8);
           }
-        }
-        if (c + kCh >= cols) {        // the accumulator is read: the next tile may have it
-          tc_fence_before_sync();
-          if (PAIR && !leader)
-            mbar_arrive_cluster(mapa_shared(smem_u32(&tempty_bar[acc]), 0));
-          else
-            mbar_arrive(smem_u32(&tempty_bar[acc]));
-        }
-        // this set's previous stores (kSets chunks ago) have read it
-        if (storer) bulk_wait_read<Cfg::kSets - 1>();
-        __syncwarp();
-        epilogue_barrier();
+          release();
+          set_free();
 #pragma unroll
-        for (int o = 0; o < Cfg::kOuts; ++o) {
-          if (EPI == kGemmGluForward && o > 0 && !P.save) break;
-#pragma unroll
-          for (int v = 0; v < kCh / 8; ++v)
-            st_shared_16(buf + o * Cfg::kBufBytes + staged<kCh>(r, v), packed[o][v]);
+          for (int v = 0; v < 8; ++v) st_shared_16(buf + staged<kRowBytes>(r, v), packed[v]);
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         epilogue_barrier();
         if (storer) {
           if (rows0 < q.M) {
 #pragma unroll
-            for (int o = 0; o < Cfg::kOuts; ++o) {
-              if (EPI == kGemmGluForward && o > 0 && !P.save) break;
-              tma_store_2d(&maps.m[q.map_out[o]], buf + o * Cfg::kBufBytes, col0 + c, rows0);
-            }
+            for (int o = 0; o < Cfg::kOuts; ++o)
+              tma_store_2d(&maps.m[q.map_out[o]], buf + Cfg::out_at(o), col0 + c, rows0);
           }
           bulk_commit();
         }

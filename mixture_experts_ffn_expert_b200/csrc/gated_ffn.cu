@@ -58,7 +58,7 @@ cudaError_t set_stream_smem() {
 }
 
 template <typename T, int EPI>
-cudaError_t set_smem() {
+cudaError_t set_dense_smem() {
   cudaError_t e = cudaFuncSetAttribute(moe::dense_gemm_kernel<T, EPI, true>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        int(moe::DenseCfg<EPI>::kSmem));
@@ -66,7 +66,18 @@ cudaError_t set_smem() {
     e = cudaFuncSetAttribute(moe::dense_gemm_kernel<T, EPI, false>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                              int(moe::DenseCfg<EPI>::kSmem));
-  if (e == cudaSuccess) e = set_stream_smem<T, EPI>();
+  return e;
+}
+
+template <typename T>
+cudaError_t set_smem() {
+  cudaError_t e = set_dense_smem<T, moe::kGemmPlain>();
+  if (e == cudaSuccess) e = set_dense_smem<T, moe::kGemmGluForward>();
+  if (e == cudaSuccess) e = set_dense_smem<T, moe::kGemmGluForwardSave>();
+  if (e == cudaSuccess) e = set_dense_smem<T, moe::kGemmGluBackward>();
+  if (e == cudaSuccess) e = set_stream_smem<T, moe::kGemmPlain>();
+  if (e == cudaSuccess) e = set_stream_smem<T, moe::kGemmGluForward>();
+  if (e == cudaSuccess) e = set_stream_smem<T, moe::kGemmGluBackward>();
   return e;
 }
 
@@ -88,12 +99,7 @@ int device_info(DeviceInfo** out) {
     if (major != 10 || minor != 0)
       return set_error(MOE_UNSUPPORTED, "this library is built for sm_100a only");
     if ((e = cudaGetSymbolAddress(&status, g_ops_status)) ||
-        (e = set_smem<__nv_bfloat16, moe::kGemmPlain>()) ||
-        (e = set_smem<__nv_bfloat16, moe::kGemmGluForward>()) ||
-        (e = set_smem<__nv_bfloat16, moe::kGemmGluBackward>()) ||
-        (e = set_smem<__half, moe::kGemmPlain>()) ||
-        (e = set_smem<__half, moe::kGemmGluForward>()) ||
-        (e = set_smem<__half, moe::kGemmGluBackward>()))
+        (e = set_smem<__nv_bfloat16>()) || (e = set_smem<__half>()))
       return cuda_error(e, "kernel attributes");
     if (!moe::tensor_map_encoder())
       return set_error(MOE_CUDA_ERROR, "cuTensorMapEncodeTiled is not available from the driver");
@@ -109,19 +115,25 @@ bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) &
 size_t align_up(size_t v) { return (v + 255) / 256 * 256; }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Matrix (rows, cols) of a 16-bit type, rows `ld` elements apart, in boxes of 64 (or 32)
-// columns x box_rows rows, swizzled over a box row's 128 (or 64) bytes; what a box covers
+// Matrix (rows, cols) of a type (an MOE_DTYPE_), rows `ld` elements apart, in boxes of box_cols
+// columns x box_rows rows, swizzled over a box row's 128, 64 or 32 bytes; what a box covers
 // beyond the matrix reads as zero and is not written.
-bool encode_map(CUtensorMap* m, int half, const void* base, int64_t rows, int64_t cols, int64_t ld,
+bool encode_map(CUtensorMap* m, int dtype, const void* base, int64_t rows, int64_t cols, int64_t ld,
                 int box_rows, int box_cols = 64) {
+  const int size = dtype == MOE_DTYPE_FP32 ? 4 : 2;
   cuuint64_t dims[2] = {cuuint64_t(cols), cuuint64_t(rows)};
-  cuuint64_t strides[1] = {cuuint64_t(ld) * 2};
+  cuuint64_t strides[1] = {cuuint64_t(ld) * size};
   cuuint32_t box[2] = {cuuint32_t(box_cols), cuuint32_t(box_rows)};
   cuuint32_t estr[2] = {1, 1};
   return moe::tensor_map_encoder()(
-             m, half ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
-             const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             m,
+             dtype == MOE_DTYPE_FP32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+             : dtype == MOE_DTYPE_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                       : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+             2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             box_cols * size == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+             : box_cols * size == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                     : CU_TENSOR_MAP_SWIZZLE_32B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -131,12 +143,17 @@ struct GemmLaunch {
   moe::DenseMaps maps;
   moe::DenseParams P = {};
   int n_maps = 0;
-  int half;                 // 16-bit type: 1 fp16, 0 bf16
+  int dtype;                // MOE_DTYPE_BF16 or MOE_DTYPE_FP16
   bool ok = true;
 
   int map(const void* base, int64_t rows, int64_t cols, int64_t ld, int box_rows,
           int box_cols = 64) {
-    ok = ok && encode_map(&maps.m[n_maps], half, base, rows, cols, ld, box_rows, box_cols);
+    ok = ok && encode_map(&maps.m[n_maps], dtype, base, rows, cols, ld, box_rows, box_cols);
+    return n_maps++;
+  }
+  // A saved pre-activation, fp32, stored in chunks of 16 columns.
+  int map_saved(const void* base, int64_t rows, int64_t cols) {
+    ok = ok && encode_map(&maps.m[n_maps], MOE_DTYPE_FP32, base, rows, cols, cols, 128, 16);
     return n_maps++;
   }
 
@@ -194,7 +211,7 @@ cudaError_t launch(GemmLaunch& L, const DeviceInfo& d, cudaStream_t st) {
 template <int EPI>
 cudaError_t launch_any(GemmLaunch& L, bool pair, const DeviceInfo& d, cudaStream_t st) {
   if (!L.ok) return cudaErrorInvalidValue;         // a tensor map could not be encoded
-  if (L.half)
+  if (L.dtype == MOE_DTYPE_FP16)
     return pair ? launch<__half, EPI, true>(L, d, st) : launch<__half, EPI, false>(L, d, st);
   return pair ? launch<__nv_bfloat16, EPI, true>(L, d, st)
               : launch<__nv_bfloat16, EPI, false>(L, d, st);
@@ -263,15 +280,15 @@ bool small_forward(int64_t tokens, int64_t d, int64_t f, const DeviceInfo& dev) 
 struct StreamLaunch {
   moe::StreamMaps maps;
   moe::StreamParams P = {};
-  int half;
+  int dtype;                // MOE_DTYPE_BF16 or MOE_DTYPE_FP16
   bool ok = true;
 
   int columns() const { return P.T <= 16 ? 16 : P.T <= 32 ? 32 : P.T <= 64 ? 64 : 128; }
   void weights(int i, const void* base, int64_t rows, int64_t cols, int box_rows) {
-    ok = ok && encode_map(&maps.a[i], half, base, rows, cols, cols, box_rows);
+    ok = ok && encode_map(&maps.a[i], dtype, base, rows, cols, cols, box_rows);
   }
   void tokens(int i, const void* base, int64_t cols, int64_t ld) {
-    ok = ok && encode_map(&maps.b[i], half, base, P.T, cols, ld, columns());
+    ok = ok && encode_map(&maps.b[i], dtype, base, P.T, cols, ld, columns());
   }
 };
 
@@ -291,7 +308,7 @@ template <int EPI>
 cudaError_t launch_stream(StreamLaunch& L, const DeviceInfo& d, cudaStream_t st) {
   if (!L.ok) return cudaErrorInvalidValue;         // a tensor map could not be encoded
   const int nb = L.columns();
-  if (L.half) {
+  if (L.dtype == MOE_DTYPE_FP16) {
     if (nb == 16) return launch_stream_columns<__half, EPI, 16>(L, d, st);
     if (nb == 32) return launch_stream_columns<__half, EPI, 32>(L, d, st);
     if (nb == 64) return launch_stream_columns<__half, EPI, 64>(L, d, st);
@@ -357,7 +374,7 @@ size_t moe_gated_ffn_workspace_bytes(int64_t T, int64_t d, int64_t f, int backwa
 
 int moe_gated_ffn_forward(int act, int dtype, int64_t T, int64_t d, int64_t f, const void* x,
                           int64_t ldx, const void* W1, const void* W3, const void* W2, void* out,
-                          int64_t ldo, void* gate, void* up, void* workspace,
+                          int64_t ldo, float* gate, float* up, void* workspace,
                           size_t workspace_bytes, void* stream) {
   if (int s = check_shape(act, dtype, T, d, f)) return s;
   if (T == 0) return MOE_OK;
@@ -377,14 +394,13 @@ int moe_gated_ffn_forward(int act, int dtype, int64_t T, int64_t d, int64_t f, c
   if (int s = device_info(&dev)) return s;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int m = int(T);
-  const int half = dtype == MOE_DTYPE_FP16;
   cudaError_t e;
   bool overlapped = false;       // the first kernel lets the second load weights early
   const bool small = small_forward(T, d, f, *dev);
   const Shape first = small ? kSingle : choose(T, f, ceil_div(d, 64), true, *dev);
   if (first == kStream) {
     StreamLaunch L;
-    L.half = half;
+    L.dtype = dtype;
     L.P.T = m;
     L.P.N = int(f);
     L.P.kb[0] = int(ceil_div(d, 64));
@@ -399,24 +415,24 @@ int moe_gated_ffn_forward(int act, int dtype, int64_t T, int64_t d, int64_t f, c
     overlapped = true;
   } else {
     GemmLaunch L;
-    L.half = half;
+    L.dtype = dtype;
     const bool pair = first == kPairs;
     const int a = L.map(x, T, d, ldx, 128);
     const int b1 = L.map(W1, f, d, d, pair ? 128 : 64);
     const int b3 = L.map(W3, f, d, d, pair ? 128 : 64);
-    const int o0 = L.map(workspace, T, f, f, 128, 32);
-    const int o1 = gate ? L.map(gate, T, f, f, 128, 32) : o0;
-    const int o2 = gate ? L.map(up, T, f, f, 128, 32) : o0;
+    const int o0 = L.map(workspace, T, f, f, 128, gate ? 16 : 32);
+    const int o1 = gate ? L.map_saved(gate, T, f) : o0;
+    const int o2 = gate ? L.map_saved(up, T, f) : o0;
     L.product(m, int(f), pair ? 256 : 128, pair ? 128 : 64, d, 0, a, a, b1, b3, 0, 0, o0, o1, o2);
-    L.P.save = gate != nullptr;
     L.P.act = act;
-    e = launch_any<moe::kGemmGluForward>(L, pair, *dev, st);
+    e = gate ? launch_any<moe::kGemmGluForwardSave>(L, pair, *dev, st)
+             : launch_any<moe::kGemmGluForward>(L, pair, *dev, st);
   }
   if (e != cudaSuccess) return cuda_error(e, "gated feed-forward gate/up launch");
   const Shape second = small ? kSingle : choose(T, d, ceil_div(f, 64), false, *dev);
   if (second == kStream) {
     StreamLaunch L;
-    L.half = half;
+    L.dtype = dtype;
     L.P.T = m;
     L.P.N = int(d);
     L.P.kb[0] = int(ceil_div(f, 64));
@@ -428,7 +444,7 @@ int moe_gated_ffn_forward(int act, int dtype, int64_t T, int64_t d, int64_t f, c
     e = launch_stream<moe::kGemmPlain>(L, *dev, st);
   } else {
     GemmLaunch L;
-    L.half = half;
+    L.dtype = dtype;
     const bool pair = second == kPairs;
     const int tile = pair ? 256 : 128;
     const int a = L.map(workspace, T, f, f, 128), b = L.map(W2, d, f, f, 128);
@@ -441,7 +457,7 @@ int moe_gated_ffn_forward(int act, int dtype, int64_t T, int64_t d, int64_t f, c
 
 int moe_gated_ffn_backward(int act, int dtype, int64_t T, int64_t d, int64_t f, const void* dout,
                            int64_t lddout, const void* x, int64_t ldx, const void* W1,
-                           const void* W3, const void* W2, const void* gate, const void* up,
+                           const void* W3, const void* W2, const float* gate, const float* up,
                            void* dx, int64_t lddx, void* dW1, void* dW3, void* dW2,
                            void* workspace, size_t workspace_bytes, void* stream) {
   if (int s = check_shape(act, dtype, T, d, f)) return s;
@@ -478,20 +494,19 @@ int moe_gated_ffn_backward(int act, int dtype, int64_t T, int64_t d, int64_t f, 
   char* ws = static_cast<char*>(workspace);
   void *dgate = ws, *dup = ws + plane, *hidden = ws + 2 * plane;
   const int m = int(T);
-  const int half = dtype == MOE_DTYPE_FP16;
   cudaError_t e;
   bool overlapped = false;       // the first kernel lets the second load weights early
   const Shape first = choose(T, f, ceil_div(d, 64), false, *dev);
   if (first == kStream) {
     StreamLaunch L;
-    L.half = half;
+    L.dtype = dtype;
     L.P.T = m;
     L.P.N = int(f);
     L.P.kb[0] = int(ceil_div(d, 64));
     L.P.a_mn = 1;
     L.P.act = act;
-    L.P.gate = const_cast<void*>(gate);
-    L.P.up = const_cast<void*>(up);
+    L.P.gate = const_cast<float*>(gate);
+    L.P.up = const_cast<float*>(up);
     L.P.dgate = dgate;
     L.P.dup = dup;
     L.P.hidden = hidden;
@@ -501,7 +516,7 @@ int moe_gated_ffn_backward(int act, int dtype, int64_t T, int64_t d, int64_t f, 
     overlapped = true;
   } else {
     GemmLaunch L;
-    L.half = half;
+    L.dtype = dtype;
     const bool pair = first == kPairs;
     const int tile = pair ? 256 : 128;
     const int a = L.map(dout, T, d, lddout, 128), b = L.map(W2, d, f, f, 64);
@@ -525,7 +540,7 @@ int moe_gated_ffn_backward(int act, int dtype, int64_t T, int64_t d, int64_t f, 
   const bool stream_dx = dx && third == kStream && (!weights || T <= 32);
   if (stream_dx) {
     StreamLaunch L;
-    L.half = half;
+    L.dtype = dtype;
     L.P.T = m;
     L.P.N = int(d);
     L.P.kb[0] = L.P.kb[1] = int(ceil_div(f, 64));
@@ -542,7 +557,7 @@ int moe_gated_ffn_backward(int act, int dtype, int64_t T, int64_t d, int64_t f, 
     if (!weights) return MOE_OK;
   }
   GemmLaunch L;
-  L.half = half;
+  L.dtype = dtype;
   const bool pair = weights ? use_pairs(f, d, T, *dev) : third == kPairs;
   const int tile = pair ? 256 : 128;
   if (dx && !stream_dx) {

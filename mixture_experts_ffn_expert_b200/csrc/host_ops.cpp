@@ -319,16 +319,16 @@ PyObject* gated_ffn_forward(PyObject*, PyObject* const* a, Py_ssize_t given) {
     at::Tensor gate, up;
     const bool save = truth(a[5]);
     if (save) {
-      gate = at::empty({T, w.f}, x.options());
-      up = at::empty({T, w.f}, x.options());
+      gate = at::empty({T, w.f}, x.options().dtype(at::kFloat));
+      up = at::empty({T, w.f}, x.options().dtype(at::kFloat));
     }
     const size_t bytes = moe_gated_ffn_workspace_bytes(T, w.d, w.f, 0);
     const at::Tensor ws = bytes_on(x, bytes);
     launch(x, [&](void* stream) {
       return moe_gated_ffn_forward(act, dt, T, w.d, w.f, x2.data_ptr(), x2.stride(0),
                                    w.w1.data_ptr(), w.w3.data_ptr(), w.w2.data_ptr(),
-                                   out.data_ptr(), w.d, ptr(gate), ptr(up), ws.data_ptr(), bytes,
-                                   stream);
+                                   out.data_ptr(), w.d, static_cast<float*>(ptr(gate)),
+                                   static_cast<float*>(ptr(up)), ws.data_ptr(), bytes, stream);
     });
     return save ? wrap_all(out, gate, up) : wrap(out);
   });
@@ -337,10 +337,10 @@ PyObject* gated_ffn_forward(PyObject*, PyObject* const* a, Py_ssize_t given) {
 const at::Tensor& saved_rows(PyObject* o, const at::Tensor& x, int64_t T, int64_t f,
                              const char* what) {
   const at::Tensor& t = cuda_tensor(o, what);
-  if (t.dim() != 2 || t.size(0) != T || t.size(1) != f || t.scalar_type() != x.scalar_type() ||
+  if (t.dim() != 2 || t.size(0) != T || t.size(1) != f || t.scalar_type() != at::kFloat ||
       t.get_device() != x.get_device() || !t.is_contiguous())
-    refuse(std::string(what) + " must be the contiguous (" + std::to_string(T) + ", " +
-           std::to_string(f) + ") tensor of gated_ffn_forward");
+    refuse(std::string(what) + " must be the contiguous fp32 (" + std::to_string(T) +
+           ", " + std::to_string(f) + ") tensor of gated_ffn_forward");
   return t;
 }
 
@@ -366,9 +366,10 @@ PyObject* gated_ffn_backward(PyObject*, PyObject* const* a, Py_ssize_t given) {
     launch(x, [&](void* stream) {
       return moe_gated_ffn_backward(act, dt, T, w.d, w.f, dout2.data_ptr(), dout2.stride(0),
                                     x2.data_ptr(), x2.stride(0), w.w1.data_ptr(),
-                                    w.w3.data_ptr(), w.w2.data_ptr(), gate.data_ptr(),
-                                    up.data_ptr(), ptr(dx), w.d, ptr(d1), ptr(d3), ptr(d2),
-                                    ws.data_ptr(), bytes, stream);
+                                    w.w3.data_ptr(), w.w2.data_ptr(),
+                                    static_cast<const float*>(gate.data_ptr()),
+                                    static_cast<const float*>(up.data_ptr()), ptr(dx), w.d,
+                                    ptr(d1), ptr(d3), ptr(d2), ws.data_ptr(), bytes, stream);
     });
     return wrap_all(dx, d1, d3, d2);
   });

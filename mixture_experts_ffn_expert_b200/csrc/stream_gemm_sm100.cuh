@@ -52,7 +52,8 @@ struct StreamParams {
   int act;
   void* out;                // plain: (T, N), rows ldo apart
   long long ldo;
-  void *gate, *up, *hidden, *dgate, *dup;
+  float *gate, *up;         // the saved pre-activations (T, N); gate/up: null to save none
+  void *hidden, *dgate, *dup;
   int test_withhold;        // test hook: block 0 withholds its first stage's weights
   int* status;
 };
@@ -300,18 +301,14 @@ __global__ void __launch_bounds__(kStreamThreads, 2)
       *reinterpret_cast<uint2*>(static_cast<T*>(P.hidden) + at) =
           make_uint2(pack2<T>(h[0], h[1]), pack2<T>(h[2], h[3]));
       if (P.gate) {
-        *reinterpret_cast<uint2*>(static_cast<T*>(P.gate) + at) =
-            make_uint2(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]));
-        *reinterpret_cast<uint2*>(static_cast<T*>(P.up) + at) =
-            make_uint2(pack2<T>(u[0], u[1]), pack2<T>(u[2], u[3]));
+        *reinterpret_cast<float4*>(P.gate + at) = make_float4(v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<float4*>(P.up + at) = make_float4(u[0], u[1], u[2], u[3]);
       }
     } else {
       const long long at = static_cast<long long>(token0 + t) * P.N + n;
-      const uint2 g2 = *reinterpret_cast<const uint2*>(static_cast<const T*>(P.gate) + at);
-      const uint2 u2 = *reinterpret_cast<const uint2*>(static_cast<const T*>(P.up) + at);
-      const float2 ga = unpack2<T>(g2.x), gb = unpack2<T>(g2.y);
-      const float2 ua = unpack2<T>(u2.x), ub = unpack2<T>(u2.y);
-      const float gg[4] = {ga.x, ga.y, gb.x, gb.y}, uu[4] = {ua.x, ua.y, ub.x, ub.y};
+      const float4 g4 = *reinterpret_cast<const float4*>(P.gate + at);
+      const float4 u4 = *reinterpret_cast<const float4*>(P.up + at);
+      const float gg[4] = {g4.x, g4.y, g4.z, g4.w}, uu[4] = {u4.x, u4.y, u4.z, u4.w};
       float dg[4], du[4], h[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {

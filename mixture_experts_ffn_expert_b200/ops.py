@@ -146,9 +146,8 @@ def gated_ffn_forward(x: torch.Tensor, W1: torch.Tensor, W3: torch.Tensor, W2: t
 
     W1 and W3 are (f, d), W2 (d, f), contiguous and 16-byte aligned, d and f multiples of 8;
     activation is "silu" or "gelu" (tanh form). Returns out, or with ``save`` (out, gate, up):
-    the (T, f) pre-activations for ``gated_ffn_backward``. Products accumulate in fp32; the
-    hidden layer and the saved pre-activations are rounded to x's type (fp16: infinite beyond
-    65504).
+    the (T, f) fp32 pre-activations for ``gated_ffn_backward``. Products accumulate in fp32; the
+    hidden layer is rounded to x's type between them (fp16: infinite beyond 65504).
     """
     return (_MODULE or _host()).gated_ffn_forward(x, W1, W3, W2, activation, save)
 

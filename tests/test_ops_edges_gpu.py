@@ -406,9 +406,9 @@ def test_a_wait_that_runs_out_is_reported_and_the_context_recovers(make, launch)
 @pytest.mark.parametrize("act", ["silu", "gelu"])
 @pytest.mark.parametrize("dtype", ["fp16", "bf16"])
 def test_gates_beyond_their_range_have_their_gradient(T, act, dtype):
-    # One hidden column has gates of -98304, which fp16 saves as -infinity, or (bf16) of -2^70,
-    # whose square is not in fp32. act and act' are 0 there as they are at -200, so every result
-    # has the bits that gates of -200 give; at the opposite gates act' is 1 as at 200.
+    # One hidden column has gates of -98304, beyond fp16, or (bf16) of -2^70, whose square is not
+    # in fp32. act and act' are 0 there as they are at -200, so every result has the bits that
+    # gates of -200 give; at the opposite gates act' is 1 as at 200.
     d, f = (72, 136) if T < 2321 else (2088, 2632)
     x, W1, W3, W2, dout = ffn_case(T, d, f, dtype, 46)
     first, big = (2.0, 98304.0) if dtype == "fp16" else (2.0 ** 35, 2.0 ** 70)
@@ -418,9 +418,7 @@ def test_gates_beyond_their_range_have_their_gradient(T, act, dtype):
     def step(gate_value, needs):
         W1[5, 0] = gate_value / first
         out, gate, up = ops.gated_ffn_forward(x, W1, W3, W2, act, save=True)
-        want = gate_value if dtype == "bf16" or abs(gate_value) < 65504 else \
-            float("inf") * gate_value
-        assert (gate[:, 5] == want).all()
+        assert gate.dtype == up.dtype == torch.float32 and (gate[:, 5] == gate_value).all()
         return [out, *ops.gated_ffn_backward(dout, x, W1, W3, W2, gate, up, act, needs)]
 
     near = 200.0 if dtype == "fp16" else 2.0 ** 8
@@ -433,10 +431,31 @@ def test_gates_beyond_their_range_have_their_gradient(T, act, dtype):
     assert torch.isfinite(dx).all()
     W1[5, 0] = 0
     gate, up = ops.gated_ffn_forward(x, W1, W3, W2, act, save=True)[1:]
-    gate[:, 5] = -near
-    W1[5, 0] = -big / first
-    assert torch.equal(dx, ops.gated_ffn_backward(dout, x, W1, W3, W2, gate, up, act,
-                                                  (True, False, False, False))[0])
+    for infinite in (-float("inf"), -near):          # the limit, and as at -200
+        gate[:, 5] = infinite
+        W1[5, 0] = -big / first
+        assert torch.equal(dx, ops.gated_ffn_backward(dout, x, W1, W3, W2, gate, up, act,
+                                                      (True, False, False, False))[0])
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("T,d,f", [(24, 2048, 2816), (100, 520, 520), (333, 2048, 1408),
+                                   (2321, 2088, 2632)])
+def test_gradients_have_one_rounding_beside_their_own(T, d, f, dtype, act):
+    # out, dW and dx each round one operand of their last product (h, dgate, dup) and the result:
+    # two roundings of one size that do not know of each other, sqrt(2) of what rounding the exact
+    # result gives; 1.5 leaves 6% for the reductions' fp32
+    x, W1, W3, W2, dout = ffn_case(T, d, f, dtype, 51)
+    out, gate, up = ops.gated_ffn_forward(x, W1, W3, W2, act, save=True)
+    assert gate.dtype == up.dtype == torch.float32
+    got = [out, *ops.gated_ffn_backward(dout, x, W1, W3, W2, gate, up, act)]
+    ax, a1, a3, a2, ad = (f64(t) for t in (x, W1, W3, W2, dout))
+    want = [O.gated_ffn(ax, a1, a3, a2, act)[0], *O.gated_ffn_grad(ad, ax, a1, a3, a2, act)]
+    for name, t, ref in zip(("out", "dx", "dW1", "dW3", "dW2"), got, want):
+        rounded = f64(torch.from_numpy(ref).to(t.dtype))
+        off, once = np.linalg.norm(f64(t) - ref), np.linalg.norm(rounded - ref)
+        assert off <= 1.5 * once, f"{name}: {off / once} roundings"
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
