@@ -464,8 +464,8 @@ __global__ void __launch_bounds__(kDgThreads, 1)
       const int col0 = tc.n * kOutCols;
       const uint32_t tbase = lane_base + static_cast<uint32_t>(acc * kAcc);
       const int cols = min(kOutCols, q.N - col0);
-      // dh: the saved pre-activations of a chunk are loaded one chunk ahead, 8 columns (v) at
-      // a time as the present chunk's are used
+      // dh: the saved pre-activations of a chunk are loaded one chunk ahead, after the present
+      // chunk's have all been used
       float4 g4[8], u4[8];
       auto load_saved = [&](int c, int v) {
         const long long at = row * q.N + col0 + c + v * 8;
@@ -567,7 +567,7 @@ __global__ void __launch_bounds__(kDgThreads, 1)
           tmem_ld_32cols(tbase + c, a);
           tmem_ld_wait();
           release();
-          set_free();
+          uint4 pk[3][4];
 #pragma unroll
           for (int v = 0; v < 4; ++v) {
             float dg[8], du[8], h[8];
@@ -584,11 +584,21 @@ __global__ void __launch_bounds__(kDgThreads, 1)
               du[j] = dh * val;
               h[j] = val * u;
             }
-            if (c + kCh < cols) load_saved(c + kCh, v);
+            pk[0][v] = pack8<T>(h);
+            pk[1][v] = pack8<T>(dg);
+            pk[2][v] = pack8<T>(du);
+          }
+          if (c + kCh < cols) {
+#pragma unroll
+            for (int v = 0; v < 4; ++v) load_saved(c + kCh, v);
+          }
+          set_free();
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
             const uint32_t at = buf + staged<kRowBytes>(r, v);
-            st_shared_16(at, pack8<T>(h));
-            st_shared_16(at + Cfg::out_at(1), pack8<T>(dg));
-            st_shared_16(at + Cfg::out_at(2), pack8<T>(du));
+            st_shared_16(at, pk[0][v]);
+            st_shared_16(at + Cfg::out_at(1), pk[1][v]);
+            st_shared_16(at + Cfg::out_at(2), pk[2][v]);
           }
         } else {
           uint4 packed[8];
