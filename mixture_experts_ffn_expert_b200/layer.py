@@ -31,8 +31,8 @@ class _NoBackward(torch.autograd.Function):
     (or a forward-mode tangent) it raises, where a plain result would hold none in silence."""
 
     @staticmethod
-    def forward(ctx, out, *inputs):
-        return out.view_as(out)
+    def forward(ctx, result, *inputs):
+        return result()               # (no tensor argument: the output is no view of one)
 
     @staticmethod
     def backward(ctx, *grads):
@@ -174,7 +174,7 @@ class MoELayer:
         inputs = [t for t in (x, norm_weight, norm_bias) if t is not None]
         if (torch.is_grad_enabled() and any(t.requires_grad for t in inputs)) \
                 or _has_tangent(*inputs):
-            return _NoBackward.apply(out, *inputs)
+            return _NoBackward.apply(lambda: out, *inputs)
         return out
 
     def routing(self) -> Dict[str, torch.Tensor]:

@@ -94,6 +94,9 @@ def test_block_around_the_layer_refuses_gradients(monkeypatch):
         assert out.requires_grad and torch.equal(out, x * 4)
         with pytest.raises(MoEError, match="no backward pass"):
             out.sum().backward()
+        out = layer.block(*args)
+        out += 1                                  # the result is the caller's, no view
+        assert torch.equal(out, x * 4 + 1)
         with torch.no_grad():
             assert not layer.block(*args).requires_grad
     for mode in (torch.no_grad, torch.enable_grad):
