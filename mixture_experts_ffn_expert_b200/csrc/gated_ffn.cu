@@ -234,9 +234,9 @@ int stream_ranks(int64_t tiles, int64_t kb, int sms) {
 // The weights' gradients run on CTA pairs once there are enough tiles for every pair of SMs
 // and a tile's reduction over the tokens is longer than its epilogue. The whole backward pass on
 // pairs and on single CTAs, us, for 384, 448, 512 and 640 tokens:
-//   d=4096 f=14336   303 and 312   312 and 368   314 and 386   386 and 447
-//   d=4096 f=4096    101 and 102   101 and 114   100 and 120   124 and 141
-//   d=2048 f=2816     54 and 46     54 and 48     55 and 51     55 and 56
+//   d=4096 f=14336   311 and 326   324 and 381   324 and 399   400 and 463
+//   d=4096 f=4096    103 and 107   105 and 118   103 and 122   128 and 146
+//   d=2048 f=2816     56 and 48     56 and 50     57 and 53     57 and 59
 // so one switch point for all sizes lies between what wide and what narrow blocks would take.
 bool use_pairs(int64_t f, int64_t d, int64_t tokens, const DeviceInfo& dev) {
   return tokens > 448 && 3 * ceil_div(f, 256) * ceil_div(d, 256) >= dev.sms / 2;
@@ -257,11 +257,11 @@ Shape choose(int64_t tokens, int64_t n, int64_t kb, bool glu, const DeviceInfo& 
 
 // Whether a forward over 65 to 128 tokens runs on single CTAs: its matrices are so small that
 // the exchange after both split reductions, 0.045 us a token each, costs more than they save
-// (128 tokens, d=f=1024: 14.5 us, 17.2 streamed; d=2048 f=1408: 20.4 and 23.1; d=7168, f=2048:
+// (128 tokens, d=f=1024: 14.5 us, 17.9 streamed; d=2048 f=1408: 20.3 and 23.7; d=7168, f=2048:
 // 43.9 and 36.6). The estimate must be 1 us ahead: where the two come out equal, streaming is the
-// faster (128 tokens, d=2048, f=2816: 26.1 us, 23.7 streamed). It holds for the 128-column tile
+// faster (128 tokens, d=2048, f=2816: 26.0 us, 23.9 streamed). It holds for the 128-column tile
 // only: up to 64 tokens the rows received have an area of their own, and streaming is ahead at
-// every size measured (64 tokens, d=f=512: 9.8 us, 8.2 streamed; d=f=1024: 14.2 and 10.8).
+// every size measured (64 tokens, d=f=512: 9.8 us, 8.2 streamed; d=f=1024: 14.1 and 11.2).
 bool small_forward(int64_t tokens, int64_t d, int64_t f, const DeviceInfo& dev) {
   if (tokens <= 64 || tokens > moe::kStreamTokens) return false;
   double single = 0.0, stream = 0.0;
@@ -534,8 +534,8 @@ int moe_gated_ffn_backward(int act, int dtype, int64_t T, int64_t d, int64_t f, 
   // dx runs in one launch with the weights' gradients, its long tiles beside their short
   // ones, unless there are so few tokens that reading W1 and W3 is all it does. The backward pass
   // streamed and together, us, for 16, 32, 64 and 128 tokens:
-  //   d=4096 f=14336   172 and 181   175 and 183   182 and 186   196 and 194
-  //   d=7168 f=2048     54 and 58     55 and 53     60 and 56     68 and 61
+  //   d=4096 f=14336   173 and 180   170 and 181   182 and 184   194 and 192
+  //   d=7168 f=2048     54 and 58     55 and 53     59 and 56     68 and 61
   //   d=2048 f=1408     18 and 19     19 and 19     22 and 21     30 and 24
   const bool stream_dx = dx && third == kStream && (!weights || T <= 32);
   if (stream_dx) {
