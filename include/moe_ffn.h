@@ -317,8 +317,8 @@ enum { MOE_ACT_SILU = 0, MOE_ACT_GELU = 1 };
  * RMS-normalised.) weight (cols) and bias (cols) may be NULL (1 and 0) and have
  * x's dtype or fp32 (wdtype); an RMS norm takes no bias. mean and rstd (rows,
  * fp32) are written when non-NULL, for the backward pass (mean: layer norm
- * only). Statistics and sums are fp32, the mean summed from the row's first
- * element, so that rows far from zero lose nothing; one rounding, on the store.
+ * only). Statistics and sums are fp32, the mean summed from one of the row's
+ * elements, so that rows far from zero lose nothing; one rounding, on the store.
  * Any cols up to 2^24, any row strides >= cols, any element-aligned pointers;
  * 16-byte aligned rows run faster. y may be x itself (equal strides). */
 int moe_norm_forward(int kind, int dtype, int wdtype, int64_t rows, int64_t cols,

@@ -11,7 +11,8 @@
 // reads x and dy and writes dx, once each. A row is held in registers (few rows) or shared
 // memory (many) between its statistics and its output; only rows too long for either are
 // read again. Statistics, products and sums are fp32. The mean is summed as differences
-// from the row's first element, p: mean = p + sum(x - p) / cols. A sum of the elements
+// from an element of the row, p, the median of its first, middle and last (so that one element
+// far from the others is not taken): mean = p + sum(x - p) / cols. A sum of the elements
 // themselves is off by several steps of a large mean, and of a constant row of 123456.79 made
 // 0.93 instead of 0; the differences' sum is off by parts of the row's spread only, so the
 // mean is, but for that, the nearest fp32 value. The variance is the mean of squared
@@ -77,10 +78,16 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// The value that a row's elements are taken from while its mean is summed: its first element
-// (0 where that is no number, so that the mean of a row with an infinity is what its sum says).
-__device__ __forceinline__ float row_pivot(float first) {
-  return isfinite(first) ? first : 0.0f;
+// The value that a row's elements are taken from while its mean is summed: the median of three
+// of them (0 where that is no number, so that the mean of a row with an infinity is what its sum
+// says).
+__device__ __forceinline__ float row_pivot(float a, float b, float c) {
+  const float p = fmaxf(fminf(a, b), fminf(fmaxf(a, b), c));
+  return isfinite(p) ? p : 0.0f;
+}
+template <typename T>
+__device__ __forceinline__ float row_pivot(const T* x, int cols) {
+  return row_pivot(to_f32(x[0]), to_f32(x[cols >> 1]), to_f32(x[cols - 1]));
 }
 
 // Sum over the `threads` threads of one row group (a multiple of 32; named barrier
@@ -120,7 +127,7 @@ __global__ void __launch_bounds__(1024) norm_forward_kernel(const NormParams P, 
   float mean = 0.0f;
   const float n = static_cast<float>(P.cols);
   if (!P.rms) {
-    const float pivot = row_pivot(to_f32(x[0]));
+    const float pivot = row_pivot(x, P.cols);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int col = (i * group + tid) * VEC;
@@ -179,7 +186,7 @@ __global__ void __launch_bounds__(1024) norm_forward_long_kernel(const NormParam
     float mean = 0.0f;
     if (!P.rms) {
       float sum = 0.0f;
-      const float pivot = row_pivot(to_f32(x[0]));
+      const float pivot = row_pivot(x, P.cols);
       for (int c = threadIdx.x; c < P.cols; c += blockDim.x) sum += to_f32(x[c]) - pivot;
       mean = pivot + group_sum(sum, s_sum[0], warp, blockDim.x, 1) / n;
     }
@@ -545,10 +552,12 @@ __device__ __forceinline__ void ld_tile(f32x2 (&f)[pairs<VEC>()], uint32_t addr)
 }
 // The pivot of the row that starts at a shared-memory address.
 template <typename T>
-__device__ __forceinline__ float tile_pivot(uint32_t row) {
-  f32x2 first[1];
-  ld_tile<T, 1>(first, row);
-  return row_pivot(first[0].x);
+__device__ __forceinline__ float tile_pivot(uint32_t row, int cols) {
+  f32x2 a[1], b[1], c[1];
+  ld_tile<T, 1>(a, row);
+  ld_tile<T, 1>(b, row + (cols >> 1) * static_cast<uint32_t>(sizeof(T)));
+  ld_tile<T, 1>(c, row + (cols - 1) * static_cast<uint32_t>(sizeof(T)));
+  return row_pivot(a[0].x, b[0].x, c[0].x);
 }
 template <typename T, int VEC>
 __device__ __forceinline__ void st_out(T* p, const f32x2 (&f)[pairs<VEC>()]) {
@@ -710,7 +719,7 @@ __global__ void __launch_bounds__(tile_threads(CW), 1)
         const uint32_t x = base + s * L.slot_bytes + tile_shift<T, VEC>(P, row0) + r * row_bytes;
         float sum = 0.0f, part_mean = 0.0f;
         if (!RMS) {
-          pivot = tile_pivot<T>(x - (q * 32 + lane) * kVecBytes);
+          pivot = tile_pivot<T>(x - (q * 32 + lane) * kVecBytes, P.cols);
           const f32x2 from = make2(-pivot, VEC == 1 ? 0.0f : -pivot);
           f32x2 acc[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
           auto add = [&](int k) {

@@ -64,6 +64,28 @@ def test_nearly_constant_rows(rows, cols):
     close(y, want, tol, "y")
 
 
+@pytest.mark.parametrize("rows,cols", NORM_KERNELS)
+def test_one_element_far_from_the_others(rows, cols):
+    # A row's mean is summed as differences from the median p of three of its elements: it is off
+    # by K U32 of the differences' mean size and by half a step of itself, which is small where p
+    # is one of the ordinary elements, wherever the far one stands.
+    g = gen(rows + 13 * cols)
+    x = torch.randn((rows, cols), generator=g)
+    far = [0, cols // 2, cols - 1, min(17, cols - 1)]
+    for row in range(rows):
+        x[row, far[row % 4]] = 1e6 * (1 - 2 * (row // 4 % 2))
+    y, mean, rstd = (f64(t) for t in ops.norm_forward(x.cuda(), save=True))
+    x = x.double().numpy()
+    want, m, r = O.norm(x)
+    p = np.median(x[:, [0, cols // 2, cols - 1]], axis=1)
+    e = K * U32 * np.abs(x - p[:, None]).mean(1) + U32 * np.abs(m) * (1 + 2 * U32)
+    assert (np.abs(mean - m) <= e).all()
+    # the variance moves by e^2 and K U32 of itself
+    er = (e * r) ** 2 / 2 + K * U32
+    assert (np.abs(rstd / r - 1) <= er).all()
+    close(y, want, (r * e)[:, None] + np.abs(want) * (er + 4 * U32)[:, None] + 1e-30, "y")
+
+
 @pytest.mark.parametrize("kind", ["layer", "rms"])
 @pytest.mark.parametrize("rows,cols", NORM_KERNELS)
 def test_inverse_deviation_over_the_range(rows, cols, kind):
